@@ -26,6 +26,13 @@ PAD_REFLECT = 1
 BF16 = 0
 FP8_E4M3 = 1
 
+ELT_BF16 = 0
+ELT_FP16 = 1
+ELT_FP32 = 2
+
+GRAD_NORM_L2 = 0
+GRAD_NORM_INF = 1
+
 EPI_BIAS = 1
 EPI_RESIDUAL = 2
 EPI_L2NORM_SILU = 4
@@ -41,7 +48,11 @@ EXPORTED = ("conv3d_packed_weight_bytes", "conv3d_pack_weight", "conv3d_output_d
             "conv3d_padded_workspace_bytes", "conv3d_fwd_padded", "conv3d_stream_pack_input",
             "conv3d_pack_weight_2d", "conv3d_norm_silu", "conv3d_packed_weight_bytes_fp8",
             "conv3d_pack_weight_fp8", "conv3d_fwd_noalloc", "conv3d_gn_partials_bytes",
-            "conv3d_fwd_gn_stats", "conv3d_group_norm_from_partials")
+            "conv3d_fwd_gn_stats", "conv3d_group_norm_from_partials",
+            "conv3d_group_norm_train_workspace_bytes", "conv3d_group_norm_train_fwd",
+            "conv3d_group_norm_train_bwd", "conv3d_norm_silu_bwd_workspace_bytes",
+            "conv3d_norm_silu_bwd", "conv3d_grad_workspace_bytes", "conv3d_grad_norm",
+            "conv3d_grad_clip")
 
 
 class Conv3dError(RuntimeError):
@@ -75,6 +86,19 @@ class conv3d_group_norm_desc(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int), ("d", ctypes.c_int), ("h", ctypes.c_int), ("w", ctypes.c_int),
                 ("c", ctypes.c_int), ("groups", ctypes.c_int), ("t_isolated", ctypes.c_int),
                 ("silu", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
+class conv3d_group_norm_train_desc(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int), ("d", ctypes.c_int), ("h", ctypes.c_int), ("w", ctypes.c_int),
+                ("c", ctypes.c_int), ("groups", ctypes.c_int), ("t_isolated", ctypes.c_int),
+                ("silu", ctypes.c_int), ("eps", ctypes.c_float), ("dtype", ctypes.c_int),
+                ("x_pitch", ctypes.c_longlong), ("y_pitch", ctypes.c_longlong),
+                ("dx_pitch", ctypes.c_longlong)]
+
+
+class conv3d_grad(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_longlong),
+                ("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int)]
 
 
 _lib = None
@@ -135,6 +159,24 @@ def lib():
         L.conv3d_fwd_gn_stats.argtypes = [pd, vp, vp, vp, vp, vp, sz, vp]
         L.conv3d_group_norm_from_partials.restype = i
         L.conv3d_group_norm_from_partials.argtypes = [pg, pd, vp, vp, vp, vp, vp, vp, sz, vp]
+        pt = ctypes.POINTER(conv3d_group_norm_train_desc)
+        L.conv3d_group_norm_train_workspace_bytes.restype = i
+        L.conv3d_group_norm_train_workspace_bytes.argtypes = [pt, i, ctypes.POINTER(sz)]
+        L.conv3d_group_norm_train_fwd.restype = i
+        L.conv3d_group_norm_train_fwd.argtypes = [pt, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.conv3d_group_norm_train_bwd.restype = i
+        L.conv3d_group_norm_train_bwd.argtypes = [pt, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.conv3d_norm_silu_bwd_workspace_bytes.restype = i
+        L.conv3d_norm_silu_bwd_workspace_bytes.argtypes = [i, i, i, i, i, ctypes.POINTER(sz)]
+        L.conv3d_norm_silu_bwd.restype = i
+        L.conv3d_norm_silu_bwd.argtypes = [vp, vp, vp, i, i, i, i, i, vp, vp, vp, vp, vp, sz, vp]
+        pr = ctypes.POINTER(conv3d_grad)
+        L.conv3d_grad_workspace_bytes.restype = i
+        L.conv3d_grad_workspace_bytes.argtypes = [pr, i, ctypes.POINTER(sz)]
+        L.conv3d_grad_norm.restype = i
+        L.conv3d_grad_norm.argtypes = [pr, i, i, vp, vp, sz, vp]
+        L.conv3d_grad_clip.restype = i
+        L.conv3d_grad_clip.argtypes = [pr, i, i, ctypes.c_float, vp, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -420,3 +462,88 @@ def conv3d_norm_silu(x, n: int, d: int, h: int, w: int, c: int, epi: conv3d_epil
     _check(lib().conv3d_norm_silu(_ptr(x), n, d, h, w, c, ctypes.byref(epi),
                                   ctypes.byref(out_pad) if out_pad else None, _ptr(previous), _ptr(y),
                                   _stream(stream)), "conv3d_norm_silu")
+
+
+# --------------------------------------------------------------------------- training
+# These take the buffers as the C entry points do (raw addresses or tensors,
+# sized by the caller); layer.GroupNormTrain, layer.NormSiluBackward and
+# layer.GradClip check tensors and allocate.
+
+def make_group_norm_train_desc(x_shape: Sequence[int], groups: int, *, eps: float = 1e-5,
+                               silu: bool = False, t_isolated: bool = True, dtype: int = ELT_BF16,
+                               x_pitch: int = 0, y_pitch: int = 0,
+                               dx_pitch: int = 0) -> conv3d_group_norm_train_desc:
+    """Training GroupNorm descriptor for an NDHWC tensor of shape x_shape."""
+    n, d, h, w, c = x_shape
+    return conv3d_group_norm_train_desc(n, d, h, w, c, groups, int(bool(t_isolated)),
+                                        int(bool(silu)), eps, dtype, x_pitch, y_pitch, dx_pitch)
+
+
+def conv3d_group_norm_train_workspace_bytes(desc: conv3d_group_norm_train_desc,
+                                            backward: bool) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().conv3d_group_norm_train_workspace_bytes(ctypes.byref(desc), int(bool(backward)),
+                                                         ctypes.byref(out)),
+           "conv3d_group_norm_train_workspace_bytes")
+    return int(out.value)
+
+
+def conv3d_group_norm_train_fwd(desc: conv3d_group_norm_train_desc, x, gamma, beta, y, stats,
+                                workspace, workspace_bytes: int, stream=None) -> None:
+    _check(lib().conv3d_group_norm_train_fwd(ctypes.byref(desc), _ptr(x), _ptr(gamma), _ptr(beta),
+                                             _ptr(y), _ptr(stats), _ptr(workspace),
+                                             workspace_bytes, _stream(stream)),
+           "conv3d_group_norm_train_fwd")
+
+
+def conv3d_group_norm_train_bwd(desc: conv3d_group_norm_train_desc, dy, x, gamma, beta, stats, dx,
+                                dgamma, dbeta, workspace, workspace_bytes: int,
+                                stream=None) -> None:
+    _check(lib().conv3d_group_norm_train_bwd(ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(gamma),
+                                             _ptr(beta), _ptr(stats), _ptr(dx), _ptr(dgamma),
+                                             _ptr(dbeta), _ptr(workspace), workspace_bytes,
+                                             _stream(stream)), "conv3d_group_norm_train_bwd")
+
+
+def conv3d_norm_silu_bwd_workspace_bytes(n: int, d: int, h: int, w: int, c: int) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().conv3d_norm_silu_bwd_workspace_bytes(n, d, h, w, c, ctypes.byref(out)),
+           "conv3d_norm_silu_bwd_workspace_bytes")
+    return int(out.value)
+
+
+def conv3d_norm_silu_bwd(value, dy, dskip, n: int, d: int, h: int, w: int, c: int, gamma, dvalue,
+                         dgamma, dbias, workspace, workspace_bytes: int, stream=None) -> None:
+    _check(lib().conv3d_norm_silu_bwd(_ptr(value), _ptr(dy), _ptr(dskip), n, d, h, w, c,
+                                      _ptr(gamma), _ptr(dvalue), _ptr(dgamma), _ptr(dbias),
+                                      _ptr(workspace), workspace_bytes, _stream(stream)),
+           "conv3d_norm_silu_bwd")
+
+
+def make_grads(grads: Sequence[tuple]):
+    """Gradient list of the calls below from (grad, out, numel, dtype,
+    out_dtype) tuples (addresses, ELT_* types; out None: in place)."""
+    arr = (conv3d_grad * len(grads))()
+    for e, (g, o, numel, dtype, out_dtype) in zip(arr, grads):
+        e.grad, e.out, e.numel, e.dtype, e.out_dtype = _ptr(g), _ptr(o), numel, dtype, out_dtype
+    return arr
+
+
+def conv3d_grad_workspace_bytes(grads) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().conv3d_grad_workspace_bytes(grads, len(grads), ctypes.byref(out)),
+           "conv3d_grad_workspace_bytes")
+    return int(out.value)
+
+
+def conv3d_grad_norm(grads, norm_type: int, norm, workspace, workspace_bytes: int,
+                     stream=None) -> None:
+    _check(lib().conv3d_grad_norm(grads, len(grads), norm_type, _ptr(norm), _ptr(workspace),
+                                  workspace_bytes, _stream(stream)), "conv3d_grad_norm")
+
+
+def conv3d_grad_clip(grads, norm_type: int, max_norm: float, norm, workspace,
+                     workspace_bytes: int, stream=None) -> None:
+    _check(lib().conv3d_grad_clip(grads, len(grads), norm_type, max_norm, _ptr(norm),
+                                  _ptr(workspace), workspace_bytes, _stream(stream)),
+           "conv3d_grad_clip")

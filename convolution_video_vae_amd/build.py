@@ -35,14 +35,18 @@ def build(verbose: bool = False) -> str:
     units = [("conv3d_igemm", [f"-DCONV3D_PART={k}", f"-DCONV3D_NPARTS={IGEMM_PARTS}"],
               f"conv3d_igemm_{k}") for k in range(IGEMM_PARTS)]
     units += [("conv3d_kernels", [], "conv3d_kernels"), ("conv3d_norm", [], "conv3d_norm")]
+    units += [(name, [], name) for name in ("conv3d_gn_train", "conv3d_ns_bwd",
+                                            "conv3d_grad_clip")]
     for name, defs, oname in units:
         obj = os.path.join(BUILD, oname + ".o")
         jobs.append([HIPCC, "-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC", "-c",
                      *DEVICE_FLAGS, *defs, "-Wall", os.path.join(CSRC, name + ".hip"), "-o", obj])
         objs.append(obj)
-    aobj = os.path.join(BUILD, "conv3d_api.o")
-    jobs.append(["g++", "-O2", "-std=c++17", "-fPIC", "-c", "-Wall", "-Wextra",
-                 os.path.join(CSRC, "conv3d_api.cpp"), "-o", aobj])
+    for name in ("conv3d_api", "conv3d_train_api"):
+        obj = os.path.join(BUILD, name + ".o")
+        jobs.append(["g++", "-O2", "-std=c++17", "-fPIC", "-c", "-Wall", "-Wextra",
+                     os.path.join(CSRC, name + ".cpp"), "-o", obj])
+        objs.append(obj)
     procs = []
     for cmd in jobs:
         if verbose:
@@ -51,7 +55,7 @@ def build(verbose: bool = False) -> str:
     failed = [cmd for cmd, p in procs if p.wait() != 0]
     if failed:
         raise subprocess.CalledProcessError(1, failed[0])
-    _run([HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, aobj, "-o", OUT + ".tmp"],
+    _run([HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", OUT + ".tmp"],
          verbose)
     os.replace(OUT + ".tmp", OUT)
     return OUT

@@ -14,6 +14,7 @@
 #include <initializer_list>
 
 #include "../../include/conv3d.h"
+#include "conv3d_checks.h"
 #include "conv3d_internal.h"
 
 using namespace conv3d;
@@ -22,43 +23,11 @@ namespace {
 
 constexpr long long kMaxTensorBytes = (1LL << 31) - 64;  // 32-bit buffer offsets
 
-struct Range {
-  uintptr_t lo = 0, hi = 0;  // [lo, hi)
-  bool empty() const { return hi <= lo; }
-};
-
-Range range_of(const void* p, long long bytes) {
-  Range r;
-  if (p && bytes > 0) {
-    r.lo = (uintptr_t)p;
-    r.hi = r.lo + (uintptr_t)bytes;
-  }
-  return r;
-}
-
-bool overlaps(const Range& a, const Range& b) {
-  return !a.empty() && !b.empty() && a.lo < b.hi && b.lo < a.hi;
-}
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
 int out_extent(int in, int s, int lo, int hi) {
   const long long span = (long long)in + lo + hi - 3;
   if (span < 0) return 0;
   const long long o = span / s + 1;
   return o > 0x7fffffffLL ? 0x7fffffff : (int)o;
-}
-
-// Product of non-negative sizes, saturating at 2^62 (every size check
-// rejects far smaller values), so no size computation overflows.
-constexpr long long kSat = 1LL << 62;
-long long prod(std::initializer_list<long long> v) {
-  long long r = 1;
-  for (long long a : v) {
-    if (a <= 0) return a < 0 ? kSat : 0;
-    r = (r > kSat / a) ? kSat : r * a;
-  }
-  return r;
 }
 
 // Everything derived from a descriptor.

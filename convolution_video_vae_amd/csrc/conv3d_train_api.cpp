@@ -1,0 +1,425 @@
+// C-ABI of the training-side operators: argument checks, planning and
+// dispatch. As in conv3d_api.cpp every check runs on the host before
+// anything is enqueued.
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <initializer_list>
+#include <vector>
+
+#include "../../include/conv3d.h"
+#include "conv3d_checks.h"
+#include "conv3d_train.h"
+
+using namespace conv3d;
+
+namespace {
+
+bool aligned_to(const void* p, int bytes) { return ((uintptr_t)p % (unsigned)bytes) == 0; }
+bool elt_ok(int t) { return t == CONV3D_ELT_BF16 || t == CONV3D_ELT_FP16 || t == CONV3D_ELT_FP32; }
+
+// ------------------------------------------------------------- GroupNorm
+
+constexpr long long kGnMaxItems = (1LL << 24) - 1;   // work-groups of one launch (grid x 256 < 2^32)
+constexpr long long kGnTarget = 2048;                // work-groups a pass aims at
+constexpr long long kGnMinChunk = 64;                // pixels; a chunk leaves 16 bytes per channel
+
+struct GnTrainPlan {
+  GnTrainArgs a;
+  size_t off_chan, off_coef, total;
+};
+
+conv3d_status plan_gn_train(const conv3d_group_norm_train_desc* d, bool bwd, GnTrainPlan* pl) {
+  if (!d) return CONV3D_ERR_NULL;
+  if (d->n <= 0 || d->d <= 0 || d->h <= 0 || d->w <= 0 || d->c <= 0 || d->groups <= 0)
+    return CONV3D_ERR_SHAPE;
+  if (!(d->eps > 0.0f) || !isfinite(d->eps)) return CONV3D_ERR_SHAPE;
+  if (d->c % d->groups) return CONV3D_ERR_SHAPE;
+  if (!elt_ok(d->dtype)) return CONV3D_ERR_UNSUPPORTED;
+  const long long xp = d->x_pitch ? d->x_pitch : d->c, yp = d->y_pitch ? d->y_pitch : d->c;
+  const long long dp = d->dx_pitch ? d->dx_pitch : d->c;
+  if (xp < d->c || yp < d->c || dp < d->c) return CONV3D_ERR_SHAPE;
+  if (d->c > 65536) return CONV3D_ERR_UNSUPPORTED;
+  const long long units = d->t_isolated ? prod({d->n, d->d}) : d->n;
+  const long long P = prod({d->t_isolated ? 1LL : (long long)d->d, d->h, d->w});
+  const int size = elt_size(d->dtype);
+  if (prod({units, P, std::max(xp, std::max(yp, dp)), size}) > (1LL << 40))
+    return CONV3D_ERR_UNSUPPORTED;
+  const long long want = std::max(1LL, (kGnTarget + units - 1) / units);
+  long long chunk = std::max((P + want - 1) / want, std::min(kGnMinChunk, P));
+  chunk = (chunk + 7) / 8 * 8;
+  const long long chunks = (P + chunk - 1) / chunk;
+  if (prod({units, chunks}) > kGnMaxItems || prod({units, d->groups}) > kGnMaxItems ||
+      chunk > (1LL << 30))
+    return CONV3D_ERR_UNSUPPORTED;
+  GnTrainArgs& a = pl->a;
+  a = GnTrainArgs{};
+  a.P = P;
+  a.C = d->c;
+  a.G = d->groups;
+  a.cpg = d->c / d->groups;
+  a.x_pitch = xp;
+  a.dy_pitch = yp;
+  a.out_pitch = bwd ? dp : yp;
+  a.units = (int)units;
+  a.chunks = (int)chunks;
+  a.chunk_px = (int)chunk;
+  a.dtype = d->dtype;
+  a.silu = d->silu ? 1 : 0;
+  a.eps = d->eps;
+  size_t at = (size_t)units * chunks * a.C * 16;
+  pl->off_chan = at = (at + 255) / 256 * 256;
+  if (bwd) {
+    at += (size_t)units * a.C * 16;
+    pl->off_coef = at = (at + 255) / 256 * 256;
+    at += (size_t)units * a.G * 8;
+  }
+  pl->total = (at + 255) / 256 * 256;
+  return CONV3D_OK;
+}
+
+// One operand: `pixels` rows of `c` elements at a pitch.
+struct Pitched {
+  Range r;
+  long long row, pitch;   // bytes
+};
+
+Pitched pitched(const void* p, long long pixels, int c, long long pitch, int size) {
+  return {range_of(p, ((pixels - 1) * pitch + c) * size), (long long)c * size, pitch * size};
+}
+
+// Whether two operands share memory. Two channel slices of one wider buffer
+// (equal pitches) are told apart although their ranges interleave.
+bool share(const Pitched& a, const Pitched& b) {
+  if (!overlaps(a.r, b.r)) return false;
+  if (a.pitch != b.pitch) return true;
+  const long long d = (long long)((b.r.lo - a.r.lo) % (uintptr_t)a.pitch);
+  const long long off = b.r.lo >= a.r.lo ? d : (a.pitch - (long long)((a.r.lo - b.r.lo) % (uintptr_t)a.pitch)) % a.pitch;
+  return off < a.row || off + b.row > a.pitch;
+}
+
+}  // namespace
+
+extern "C" {
+
+conv3d_status conv3d_group_norm_train_workspace_bytes(const conv3d_group_norm_train_desc* desc,
+                                                      int backward, size_t* bytes) {
+  if (!bytes) return CONV3D_ERR_NULL;
+  GnTrainPlan pl;
+  const conv3d_status st = plan_gn_train(desc, backward != 0, &pl);
+  if (st != CONV3D_OK) return st;
+  *bytes = pl.total;
+  return CONV3D_OK;
+}
+
+conv3d_status conv3d_group_norm_train_fwd(const conv3d_group_norm_train_desc* desc, const void* x,
+                                          const float* gamma, const float* beta, void* y,
+                                          float* stats, void* workspace, size_t workspace_bytes,
+                                          void* stream) {
+  if (!desc || !x || !gamma || !beta || !y || !stats) return CONV3D_ERR_NULL;
+  GnTrainPlan pl;
+  const conv3d_status st = plan_gn_train(desc, false, &pl);
+  if (st != CONV3D_OK) return st;
+  GnTrainArgs& a = pl.a;
+  const int size = elt_size(a.dtype);
+  if (!aligned_to(x, size) || !aligned_to(y, size) || !aligned_to(gamma, 4) ||
+      !aligned_to(beta, 4) || !aligned_to(stats, 4))
+    return CONV3D_ERR_ALIGN;
+  if (!workspace || workspace_bytes < pl.total) return CONV3D_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return CONV3D_ERR_ALIGN;
+  const long long pixels = a.units * a.P;
+  const Pitched px = pitched(x, pixels, a.C, a.x_pitch, size);
+  const Pitched py = pitched(y, pixels, a.C, a.out_pitch, size);
+  const Range rg = range_of(gamma, 4LL * a.C), rb = range_of(beta, 4LL * a.C);
+  const Range rs = range_of(stats, 8LL * a.units * a.G);
+  const Range rw = range_of(workspace, (long long)pl.total);
+  if (share(px, py)) return CONV3D_ERR_OVERLAP;
+  for (const Range& o : {rs, rw})
+    for (const Range& i : {px.r, py.r, rg, rb})
+      if (overlaps(o, i)) return CONV3D_ERR_OVERLAP;
+  if (overlaps(rs, rw) || overlaps(py.r, rg) || overlaps(py.r, rb)) return CONV3D_ERR_OVERLAP;
+  a.x = x;
+  a.out = y;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.stats = stats;
+  a.partial = (double*)workspace;
+  return launch_gn_train_fwd(a, stream) ? CONV3D_ERR_HIP : CONV3D_OK;
+}
+
+conv3d_status conv3d_group_norm_train_bwd(const conv3d_group_norm_train_desc* desc, const void* dy,
+                                          const void* x, const float* gamma, const float* beta,
+                                          const float* stats, void* dx, float* dgamma,
+                                          float* dbeta, void* workspace, size_t workspace_bytes,
+                                          void* stream) {
+  if (!desc || !dy || !x || !gamma || !beta || !stats) return CONV3D_ERR_NULL;
+  if (!dx && !dgamma && !dbeta) return CONV3D_ERR_NULL;
+  GnTrainPlan pl;
+  const conv3d_status st = plan_gn_train(desc, true, &pl);
+  if (st != CONV3D_OK) return st;
+  GnTrainArgs& a = pl.a;
+  const int size = elt_size(a.dtype);
+  if (!aligned_to(x, size) || !aligned_to(dy, size) || !aligned_to(dx, size) ||
+      !aligned_to(gamma, 4) || !aligned_to(beta, 4) || !aligned_to(stats, 4) ||
+      !aligned_to(dgamma, 4) || !aligned_to(dbeta, 4))
+    return CONV3D_ERR_ALIGN;
+  if (!workspace || workspace_bytes < pl.total) return CONV3D_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return CONV3D_ERR_ALIGN;
+  const long long pixels = a.units * a.P;
+  const Pitched px = pitched(x, pixels, a.C, a.x_pitch, size);
+  const Pitched pd = pitched(dy, pixels, a.C, a.dy_pitch, size);
+  const Range ins[] = {px.r, pd.r, range_of(gamma, 4LL * a.C), range_of(beta, 4LL * a.C),
+                       range_of(stats, 8LL * a.units * a.G)};
+  const Range small[] = {range_of(dgamma, 4LL * a.C), range_of(dbeta, 4LL * a.C),
+                         range_of(workspace, (long long)pl.total)};
+  for (int i = 0; i < 3; ++i) {
+    for (const Range& r : ins)
+      if (overlaps(small[i], r)) return CONV3D_ERR_OVERLAP;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(small[i], small[j])) return CONV3D_ERR_OVERLAP;
+  }
+  if (dx) {
+    const Pitched po = pitched(dx, pixels, a.C, a.out_pitch, size);
+    const bool in_place = dx == dy && a.out_pitch == a.dy_pitch;
+    if (share(po, px) || (!in_place && share(po, pd))) return CONV3D_ERR_OVERLAP;
+    for (const Range& r : small)
+      if (overlaps(po.r, r)) return CONV3D_ERR_OVERLAP;
+    for (int i = 2; i < 5; ++i)
+      if (overlaps(po.r, ins[i])) return CONV3D_ERR_OVERLAP;
+  }
+  a.x = x;
+  a.dy = dy;
+  a.out = dx;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.stats = const_cast<float*>(stats);
+  a.partial = (double*)workspace;
+  a.chan = (double*)((char*)workspace + pl.off_chan);
+  a.coef = (float*)((char*)workspace + pl.off_coef);
+  a.dgamma = dgamma;
+  a.dbeta = dbeta;
+  return launch_gn_train_bwd(a, stream) ? CONV3D_ERR_HIP : CONV3D_OK;
+}
+
+// ------------------------------------------------- channel norm + SiLU, backward
+
+static conv3d_status ns_bwd_check(int n, int d, int h, int w, int c, long long* M,
+                                  long long* bytes, size_t* ws) {
+  if (n <= 0 || d <= 0 || h <= 0 || w <= 0 || c <= 0) return CONV3D_ERR_SHAPE;
+  if (c % 8) return CONV3D_ERR_ALIGN;
+  if (c > 2048) return CONV3D_ERR_UNSUPPORTED;
+  *M = prod({n, d, h, w});
+  *bytes = prod({*M, c, 2});
+  if (*bytes > (1LL << 40)) return CONV3D_ERR_UNSUPPORTED;
+  *ws = ((size_t)ns_bwd_blocks(*M, c) * 2 * c * 4 + 255) / 256 * 256;
+  return CONV3D_OK;
+}
+
+conv3d_status conv3d_norm_silu_bwd_workspace_bytes(int n, int d, int h, int w, int c,
+                                                   size_t* bytes) {
+  if (!bytes) return CONV3D_ERR_NULL;
+  long long M, t;
+  return ns_bwd_check(n, d, h, w, c, &M, &t, bytes);
+}
+
+conv3d_status conv3d_norm_silu_bwd(const void* value, const void* dy, const void* dskip, int n,
+                                   int d, int h, int w, int c, const void* gamma, void* dvalue,
+                                   float* dgamma, float* dbias, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  if (!value || !dy || !gamma || !dvalue) return CONV3D_ERR_NULL;
+  long long M, bytes;
+  size_t ws;
+  const conv3d_status st = ns_bwd_check(n, d, h, w, c, &M, &bytes, &ws);
+  if (st != CONV3D_OK) return st;
+  if (!aligned16(value) || !aligned16(dy) || !aligned16(dskip) || !aligned16(gamma) ||
+      !aligned16(dvalue) || !aligned_to(dgamma, 4) || !aligned_to(dbias, 4))
+    return CONV3D_ERR_ALIGN;
+  const bool sums = dgamma || dbias;
+  if (sums && (!workspace || workspace_bytes < ws)) return CONV3D_ERR_WORKSPACE;
+  if (sums && !aligned16(workspace)) return CONV3D_ERR_ALIGN;
+  const Range rv = range_of(value, bytes), ry = range_of(dy, bytes), rs = range_of(dskip, bytes);
+  const Range rg = range_of(gamma, 2LL * c), ro = range_of(dvalue, bytes);
+  const Range outs[] = {ro, range_of(dgamma, 4LL * c), range_of(dbias, 4LL * c),
+                        sums ? range_of(workspace, (long long)ws) : Range()};
+  for (int i = 0; i < 4; ++i) {
+    const bool big = i == 0;
+    if (overlaps(outs[i], rv) || overlaps(outs[i], rg) ||
+        (!(big && dvalue == dy) && overlaps(outs[i], ry)) ||
+        (!(big && dvalue == dskip) && overlaps(outs[i], rs)))
+      return CONV3D_ERR_OVERLAP;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(outs[i], outs[j])) return CONV3D_ERR_OVERLAP;
+  }
+  NsBwdArgs a{};
+  a.value = (const uint16_t*)value;
+  a.dy = (const uint16_t*)dy;
+  a.dskip = (const uint16_t*)dskip;
+  a.gamma = (const uint16_t*)gamma;
+  a.dvalue = (uint16_t*)dvalue;
+  a.dgamma = dgamma;
+  a.dbias = dbias;
+  a.partial = (float*)workspace;
+  a.M = M;
+  a.C = c;
+  a.blocks = ns_bwd_blocks(M, c);
+  return launch_ns_bwd(a, stream) ? CONV3D_ERR_HIP : CONV3D_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------ gradient norm and clipping
+
+namespace {
+
+constexpr int kGradMaxCount = 1 << 20;
+constexpr long long kGradMaxElements = 1LL << 40;
+
+struct GradPlan {
+  long long chunk = 0;         // elements per work-group
+  long long partials = 0;      // work-groups over all tensors
+  size_t bytes = 0;
+};
+
+// Work-groups of one tensor. A pass aims at kGradTarget of them in all: each
+// leaves one partial, and each work-group of the clip pass adds all partials.
+constexpr long long kGradTarget = 1536, kGradMinChunk = 4096, kGradStep = 2048;
+
+long long grad_blocks(long long numel, long long chunk) { return (numel + chunk - 1) / chunk; }
+
+conv3d_status plan_grads(const conv3d_grad* g, int count, GradPlan* pl) {
+  if (count < 0) return CONV3D_ERR_SHAPE;
+  if (count > 0 && !g) return CONV3D_ERR_NULL;
+  if (count > kGradMaxCount) return CONV3D_ERR_UNSUPPORTED;
+  long long total = 0;
+  for (int i = 0; i < count; ++i) {
+    if (g[i].numel < 0) return CONV3D_ERR_SHAPE;
+    if (!elt_ok(g[i].dtype) || !elt_ok(g[i].out_dtype)) return CONV3D_ERR_UNSUPPORTED;
+    if (g[i].numel > kGradMaxElements || (total += g[i].numel) > kGradMaxElements)
+      return CONV3D_ERR_UNSUPPORTED;
+  }
+  pl->chunk = std::max(kGradMinChunk, (total / kGradTarget + kGradStep) / kGradStep * kGradStep);
+  for (int i = 0; i < count; ++i) pl->partials += grad_blocks(g[i].numel, pl->chunk);
+  if (pl->chunk > (1LL << 30) || pl->partials > (1LL << 24) - 1) return CONV3D_ERR_UNSUPPORTED;
+  pl->bytes = ((size_t)std::max(pl->partials, 1LL) * 8 + 255) / 256 * 256;
+  return CONV3D_OK;
+}
+
+struct Span {
+  uintptr_t lo, hi;
+  bool write;
+};
+
+// Every written range must lie apart from every other range.
+bool spans_clash(std::vector<Span>& v) {
+  std::sort(v.begin(), v.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  uintptr_t any = 0, written = 0;
+  for (const Span& s : v) {
+    if (s.lo < (s.write ? any : written)) return true;
+    any = std::max(any, s.hi);
+    if (s.write) written = std::max(written, s.hi);
+  }
+  return false;
+}
+
+conv3d_status run_grads(const conv3d_grad* g, int count, int norm_type, bool clip, float max_norm,
+                        float* norm, void* workspace, size_t workspace_bytes, void* stream) {
+  if (norm_type != CONV3D_GRAD_NORM_L2 && norm_type != CONV3D_GRAD_NORM_INF)
+    return CONV3D_ERR_UNSUPPORTED;
+  if (clip && (!(max_norm >= 0.0f) || !isfinite(max_norm))) return CONV3D_ERR_SHAPE;
+  if (!norm) return CONV3D_ERR_NULL;
+  GradPlan pl;
+  conv3d_status st = plan_grads(g, count, &pl);
+  if (st != CONV3D_OK) return st;
+  std::vector<Span> spans;
+  spans.reserve((size_t)count * 2 + 2);
+  int last = -1;                         // the last tensor that holds anything
+  for (int i = 0; i < count; ++i) {
+    if (g[i].numel == 0) continue;
+    last = i;
+    const uintptr_t src = (uintptr_t)g[i].grad;
+    if (!src) return CONV3D_ERR_NULL;
+    if (src % (unsigned)elt_size(g[i].dtype)) return CONV3D_ERR_ALIGN;
+    const bool in_place = !g[i].out || g[i].out == g[i].grad;
+    if (clip && in_place && g[i].out_dtype != g[i].dtype) return CONV3D_ERR_OVERLAP;
+    spans.push_back({src, src + (uintptr_t)g[i].numel * elt_size(g[i].dtype), clip && in_place});
+    if (clip && !in_place) {
+      const uintptr_t dst = (uintptr_t)g[i].out;
+      if (dst % (unsigned)elt_size(g[i].out_dtype)) return CONV3D_ERR_ALIGN;
+      spans.push_back({dst, dst + (uintptr_t)g[i].numel * elt_size(g[i].out_dtype), true});
+    }
+  }
+  if (!aligned_to(norm, 4)) return CONV3D_ERR_ALIGN;
+  if (!workspace || workspace_bytes < pl.bytes) return CONV3D_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return CONV3D_ERR_ALIGN;
+  spans.push_back({(uintptr_t)norm, (uintptr_t)norm + 4, true});
+  spans.push_back({(uintptr_t)workspace, (uintptr_t)workspace + pl.bytes, true});
+  if (spans_clash(spans)) return CONV3D_ERR_OVERLAP;
+
+  double* partial = (double*)workspace;
+  GradBatch b{};
+  b.all = partial;
+  b.norm = norm;
+  b.chunk = (int)pl.chunk;
+  b.partials = (int)pl.partials;
+  b.inf = norm_type == CONV3D_GRAD_NORM_INF;
+  b.max_norm = max_norm;
+  for (int pass = 0; pass < (clip ? 2 : 1); ++pass) {
+    b.partial = partial;
+    b.norm = norm;
+    b.count = b.blocks = 0;
+    for (int i = 0; i < count; ++i) {
+      if (g[i].numel == 0) continue;
+      GradItem& it = b.item[b.count++];
+      it.src = g[i].grad;
+      it.dst = g[i].out ? g[i].out : g[i].grad;
+      it.numel = g[i].numel;
+      it.first = b.blocks;
+      it.dtype = (short)g[i].dtype;
+      it.out_dtype = (short)g[i].out_dtype;
+      b.blocks += (int)grad_blocks(g[i].numel, pl.chunk);
+      if (b.count < kGradItems && i != last) continue;
+      if (pass == 0 ? launch_grad_partials(b, stream) : launch_grad_scale(b, stream))
+        return CONV3D_ERR_HIP;
+      b.partial += b.blocks;
+      b.norm = nullptr;                  // the first batch of the clip pass writes it
+      b.count = b.blocks = 0;
+    }
+  }
+  if (!clip || pl.partials == 0) {
+    b.norm = norm;
+    if (launch_grad_norm(b, stream)) return CONV3D_ERR_HIP;
+  }
+  return CONV3D_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+conv3d_status conv3d_grad_workspace_bytes(const conv3d_grad* grads, int count, size_t* bytes) {
+  if (!bytes) return CONV3D_ERR_NULL;
+  GradPlan pl;
+  const conv3d_status st = plan_grads(grads, count, &pl);
+  if (st != CONV3D_OK) return st;
+  *bytes = pl.bytes;
+  return CONV3D_OK;
+}
+
+conv3d_status conv3d_grad_norm(const conv3d_grad* grads, int count, int norm_type, float* norm,
+                               void* workspace, size_t workspace_bytes, void* stream) try {
+  return run_grads(grads, count, norm_type, false, 0.0f, norm, workspace, workspace_bytes, stream);
+} catch (...) {            // the host's memory is exhausted
+  return CONV3D_ERR_UNSUPPORTED;
+}
+
+conv3d_status conv3d_grad_clip(const conv3d_grad* grads, int count, int norm_type, float max_norm,
+                               float* norm, void* workspace, size_t workspace_bytes,
+                               void* stream) try {
+  return run_grads(grads, count, norm_type, true, max_norm, norm, workspace, workspace_bytes,
+                   stream);
+} catch (...) {
+  return CONV3D_ERR_UNSUPPORTED;
+}
+
+}  // extern "C"

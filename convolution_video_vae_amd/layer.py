@@ -11,12 +11,16 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import (NCDHW, NDHWC, conv3d_fwd, conv3d_fwd_padded, conv3d_group_norm,
-               conv3d_group_norm_workspace_bytes, conv3d_output_dims, conv3d_pack_weight,
-               conv3d_pack_weight_2d, conv3d_pack_weight_fp8, conv3d_packed_weight_bytes,
-               conv3d_packed_weight_bytes_fp8, conv3d_padded_workspace_bytes,
-               conv3d_stream_pack_input, conv3d_workspace_bytes, make_desc, make_epilogue,
-               make_group_norm_desc, make_out_pad)
+from . import (ELT_BF16, ELT_FP16, ELT_FP32, GRAD_NORM_INF, GRAD_NORM_L2, NCDHW, NDHWC,
+               conv3d_fwd, conv3d_fwd_padded, conv3d_grad_clip, conv3d_grad_norm, conv3d_grad_workspace_bytes,
+               conv3d_group_norm, conv3d_group_norm_train_bwd, conv3d_group_norm_train_fwd,
+               conv3d_group_norm_train_workspace_bytes, conv3d_group_norm_workspace_bytes,
+               conv3d_norm_silu_bwd, conv3d_norm_silu_bwd_workspace_bytes, conv3d_output_dims,
+               conv3d_pack_weight, conv3d_pack_weight_2d, conv3d_pack_weight_fp8,
+               conv3d_packed_weight_bytes, conv3d_packed_weight_bytes_fp8,
+               conv3d_padded_workspace_bytes, conv3d_stream_pack_input, conv3d_workspace_bytes,
+               make_desc, make_epilogue, make_grads, make_group_norm_desc,
+               make_group_norm_train_desc, make_out_pad)
 
 
 def _expect(t: Optional[torch.Tensor], shape, what: str) -> None:
@@ -202,3 +206,260 @@ class GroupNorm:
         conv3d_group_norm(self.desc, x, self.gamma, self.beta, y, self.workspace,
                           self.workspace_bytes, stream)
         return y
+
+
+# --------------------------------------------------------------------------- training
+# The classes below run on the current stream of their tensors' device.
+# Outputs and scratch memory that a call needs come from PyTorch's allocator
+# on that stream (inside a graph capture, from the graph's own pool), so one
+# object may serve several streams and graphs at once.
+
+_ELT = {torch.bfloat16: ELT_BF16, torch.float16: ELT_FP16, torch.float32: ELT_FP32}
+
+
+def _pixel_pitch(t: torch.Tensor) -> int:
+    """Elements between consecutive pixels of an NDHWC tensor whose channels
+    are contiguous; 0 if its pixels are not evenly spaced."""
+    c = t.shape[4]
+    if t.is_contiguous():
+        return c
+    if c > 1 and t.stride(4) != 1:
+        return 0
+    pitch, run = 0, 1
+    for i in (3, 2, 1, 0):
+        if t.shape[i] > 1:
+            if pitch == 0:
+                pitch = t.stride(i)
+                if pitch < c:
+                    return 0
+            elif t.stride(i) != pitch * run:
+                return 0
+        run *= t.shape[i]
+    return pitch or c
+
+
+def _activation(t: torch.Tensor, shape, dtype, what: str) -> int:
+    """Checks an NDHWC activation (a channel slice of a wider tensor counts)
+    and returns its pixel pitch."""
+    pitch = (_pixel_pitch(t) if t.is_cuda and t.dtype == dtype and tuple(t.shape) == shape else 0)
+    if not pitch:
+        raise ValueError(f"{what} must be a {dtype} GPU tensor of shape {shape} with contiguous "
+                         f"channels and evenly spaced pixels, got {tuple(t.shape)} {t.dtype} "
+                         f"strides {tuple(t.stride())} on {t.device}")
+    return pitch
+
+
+def _vector(t: torch.Tensor, numel: int, dtype, device, what: str) -> None:
+    if t.dtype != dtype or t.numel() != numel or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of {numel} values on "
+                         f"{device}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+
+
+def _same_device(device, **tensors) -> None:
+    for what, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{what} is on {t.device}, x on {device}")
+
+
+class GroupNormTrain:
+    """Channels-last GroupNorm (+ SiLU) of one NDHWC activation shape with its
+    backward pass: forward keeps the statistics that backward needs. Tensors
+    may be channel slices of wider ones."""
+
+    def __init__(self, x_shape: Sequence[int], groups: int, *, eps: float = 1e-5,
+                 silu: bool = False, t_isolated: bool = True, dtype=torch.bfloat16):
+        if dtype not in _ELT:
+            raise ValueError(f"dtype must be one of {list(_ELT)}, got {dtype}")
+        self.x_shape = tuple(int(v) for v in x_shape)
+        self.dtype = dtype
+        n, d, _, _, c = self.x_shape
+        self.c = c
+        self.stats_shape = (n * d if t_isolated else n, groups, 2)
+        self._stats_numel = self.stats_shape[0] * groups * 2
+        self._kw = dict(eps=eps, silu=silu, t_isolated=t_isolated, dtype=_ELT[dtype])
+        self.groups = groups
+        self._descs = {}
+        self._ws = tuple(conv3d_group_norm_train_workspace_bytes(self._desc(c, c, c), b)
+                         for b in (False, True))
+
+    def _desc(self, x_pitch: int, y_pitch: int, dx_pitch: int):
+        key = (x_pitch, y_pitch, dx_pitch)
+        d = self._descs.get(key)
+        if d is None:
+            d = self._descs[key] = make_group_norm_train_desc(
+                self.x_shape, self.groups, x_pitch=x_pitch, y_pitch=y_pitch, dx_pitch=dx_pitch,
+                **self._kw)
+        return d
+
+    def forward(self, x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor,
+                y: Optional[torch.Tensor] = None, stats: Optional[torch.Tensor] = None):
+        """(y, stats): the norm of x, and per unit and group the fp32 mean and
+        1/sqrt(var + eps). gamma and beta are fp32 [c]."""
+        dev = x.device
+        xp = _activation(x, self.x_shape, self.dtype, "x")
+        if dev.index != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return self.forward(x, gamma, beta, y, stats)
+        _vector(gamma, self.c, torch.float32, dev, "gamma")
+        _vector(beta, self.c, torch.float32, dev, "beta")
+        if y is None:
+            y = torch.empty(self.x_shape, dtype=self.dtype, device=dev)
+        if stats is None:
+            stats = torch.empty(self.stats_shape, dtype=torch.float32, device=dev)
+        else:
+            _vector(stats, self._stats_numel, torch.float32, dev, "stats")
+        yp = _activation(y, self.x_shape, self.dtype, "y")
+        _same_device(dev, y=y)
+        ws = torch.empty(self._ws[0], dtype=torch.uint8, device=dev)
+        conv3d_group_norm_train_fwd(self._desc(xp, yp, yp), x, gamma, beta, y, stats, ws,
+                                    self._ws[0])
+        return y, stats
+
+    def backward(self, dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor,
+                 beta: torch.Tensor, stats: torch.Tensor, dx: Optional[torch.Tensor] = None,
+                 need_dx: bool = True, need_params: bool = True):
+        """(dx, dgamma, dbeta) for the gradient dy of y; dx may be given (dy
+        itself included), and is None without need_dx, dgamma and dbeta
+        (fp32) without need_params."""
+        dev = x.device
+        xp = _activation(x, self.x_shape, self.dtype, "x")
+        dp = _activation(dy, self.x_shape, self.dtype, "dy")
+        if dev.index != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return self.backward(dy, x, gamma, beta, stats, dx, need_dx, need_params)
+        _vector(gamma, self.c, torch.float32, dev, "gamma")
+        _vector(beta, self.c, torch.float32, dev, "beta")
+        _vector(stats, self._stats_numel, torch.float32, dev, "stats")
+        if not need_dx:
+            if dx is not None:
+                raise ValueError("dx is given but not wanted")
+            op = self.c
+        else:
+            if dx is None:
+                dx = torch.empty(self.x_shape, dtype=self.dtype, device=dev)
+            op = _activation(dx, self.x_shape, self.dtype, "dx")
+        _same_device(dev, dy=dy, dx=dx)
+        dgamma = dbeta = None
+        if need_params:
+            dgamma = torch.empty(self.c, dtype=torch.float32, device=dev)
+            dbeta = torch.empty(self.c, dtype=torch.float32, device=dev)
+        ws = torch.empty(self._ws[1], dtype=torch.uint8, device=dev)
+        conv3d_group_norm_train_bwd(self._desc(xp, dp, op), dy, x, gamma, beta, stats, dx, dgamma,
+                                    dbeta, ws, self._ws[1])
+        return dx, dgamma, dbeta
+
+
+class NormSiluBackward:
+    """Backward pass of the channel L2 norm x sqrt(C) x gamma -> SiLU (the
+    conv's norm_silu epilogue, conv3d_norm_silu) on one NDHWC bf16 shape."""
+
+    def __init__(self, x_shape: Sequence[int], *, bias: bool = False, gamma: bool = True):
+        """bias, gamma: whether their gradients are wanted."""
+        self.x_shape = tuple(int(v) for v in x_shape)
+        self.want_bias, self.want_gamma = bias, gamma
+        self._ws = conv3d_norm_silu_bwd_workspace_bytes(*self.x_shape)
+
+    def __call__(self, value: torch.Tensor, dy: torch.Tensor, gamma: torch.Tensor,
+                 dskip: Optional[torch.Tensor] = None, dvalue: Optional[torch.Tensor] = None):
+        """(dvalue, dgamma, dbias): dvalue bf16 is the gradient of `value` (the
+        pre-norm sum: of the conv's output and of the residual alike), dgamma
+        and dbias fp32 (None where not wanted). dskip: the gradient that
+        reaches value past the norm. dvalue may be given (dy or dskip
+        included)."""
+        dev = value.device
+        _expect(value, self.x_shape, "value")
+        _expect(dy, self.x_shape, "dy")
+        _expect(dskip, self.x_shape, "dskip")
+        _expect(dvalue, self.x_shape, "dvalue")
+        _same_device(dev, dy=dy, dskip=dskip, dvalue=dvalue)
+        if dev.index != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return self(value, dy, gamma, dskip, dvalue)
+        n, d, h, w, c = self.x_shape
+        _vector(gamma, c, torch.bfloat16, dev, "gamma")
+        if dvalue is None:
+            dvalue = torch.empty_like(value)
+        dgamma = torch.empty(c, dtype=torch.float32, device=dev) if self.want_gamma else None
+        dbias = torch.empty(c, dtype=torch.float32, device=dev) if self.want_bias else None
+        ws = None
+        if self.want_gamma or self.want_bias:
+            ws = torch.empty(self._ws, dtype=torch.uint8, device=dev)
+        conv3d_norm_silu_bwd(value, dy, dskip, n, d, h, w, c, gamma, dvalue, dgamma, dbias, ws,
+                             self._ws)
+        return dvalue, dgamma, dbias
+
+
+def _dense(t: torch.Tensor) -> bool:
+    """Whether t's elements fill one run of memory, each once, in any order."""
+    if t.is_contiguous():
+        return True
+    run = 1
+    for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n != 1):
+        if stride != run:
+            return False
+        run *= size
+    return True
+
+
+class GradClip:
+    """Global norm of many gradient tensors (bf16, fp16 or fp32, mixed), and
+    clipping, in place or into `outs` (same shapes and strides, any of the
+    types). The lists are kept; a tensor whose memory has moved since the
+    last call is looked up again."""
+
+    def __init__(self, grads: Sequence[torch.Tensor],
+                 outs: Optional[Sequence[torch.Tensor]] = None, *, norm: str = "l2"):
+        if norm not in ("l2", "inf"):
+            raise ValueError(f"norm must be 'l2' or 'inf', got {norm!r}")
+        self.grads = list(grads)
+        self.outs = None if outs is None else list(outs)
+        if not self.grads:
+            raise ValueError("no gradients")
+        if self.outs is not None and len(self.outs) != len(self.grads):
+            raise ValueError(f"{len(self.grads)} gradients but {len(self.outs)} outs")
+        self._norm_type = GRAD_NORM_INF if norm == "inf" else GRAD_NORM_L2
+        self.device = self.grads[0].device
+        self._all = self.grads + (self.outs or [])
+        self._build()
+
+    def _build(self) -> None:
+        for i, t in enumerate(self._all):
+            if not t.is_cuda or t.device != self.device or t.dtype not in _ELT or not _dense(t):
+                raise ValueError(f"gradient {i % len(self.grads)} must be a dense bf16, fp16 or "
+                                 f"fp32 tensor on {self.device}, got {tuple(t.shape)} {t.dtype} "
+                                 f"strides {tuple(t.stride())} on {t.device}")
+        for i, (g, o) in enumerate(zip(self.grads, self.outs or [])):
+            if g.shape != o.shape or (g.stride() != o.stride()
+                                      and not (g.is_contiguous() and o.is_contiguous())):
+                raise ValueError(f"out {i} differs from its gradient in shape or strides")
+        self._ptrs = [t.data_ptr() for t in self._all]
+        self._table = make_grads([(g, o, g.numel(), _ELT[g.dtype], _ELT[(o if o is not None
+                                                                          else g).dtype])
+                                  for g, o in zip(self.grads, self.outs or [None] * len(self.grads))])
+        self._ws = conv3d_grad_workspace_bytes(self._table)
+
+    def _call(self, run):
+        if self.device.index != torch.cuda.current_device():
+            with torch.cuda.device(self.device):
+                return self._call(run)
+        if [t.data_ptr() for t in self._all] != self._ptrs:
+            self._build()
+        norm = torch.empty((), dtype=torch.float32, device=self.device)
+        run(norm, torch.empty(self._ws, dtype=torch.uint8, device=self.device))
+        return norm
+
+    def norm(self) -> torch.Tensor:
+        """The norm over all gradients (fp32, on the GPU); nothing is changed."""
+        return self._call(lambda norm, ws: conv3d_grad_norm(self._table, self._norm_type, norm, ws,
+                                                            self._ws))
+
+    def clip(self, max_norm: float) -> torch.Tensor:
+        """Scales every gradient by min(1, max_norm / (norm + 1e-6)) and
+        returns the norm before that (fp32, on the GPU)."""
+        return self._call(lambda norm, ws: conv3d_grad_clip(self._table, self._norm_type, max_norm,
+                                                            norm, ws, self._ws))
+
+
+def clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *, norm: str = "l2") -> torch.Tensor:
+    """Clips gradients in place by their global norm and returns it."""
+    return GradClip(grads, norm=norm).clip(max_norm)

@@ -27,7 +27,8 @@
  * Conventions for every entry point:
  *  - Tensor pointers are DEVICE pointers to bf16 data (raw 16-bit patterns),
  *    except `bias`, `gamma` and `beta` of the GroupNorm, which are fp32. All
- *    must be 16-byte aligned.
+ *    must be 16-byte aligned. The training-side entry points state their own
+ *    types and alignments.
  *  - `stream` is a hipStream_t (NULL = the default stream). Every entry point
  *    only enqueues work on `stream` and returns; nothing is synchronised.
  *  - The caller owns every buffer. The library allocates nothing, keeps no
@@ -365,6 +366,128 @@ conv3d_status conv3d_group_norm_from_partials(const conv3d_group_norm_desc* desc
                                              const void* x, const float* gamma, const float* beta,
                                              void* y, void* workspace, size_t workspace_bytes,
                                              void* stream);
+
+/* ---------------------------------------------------- training: GroupNorm
+ * GroupNorm (+ SiLU) that keeps its statistics, and its backward pass, on
+ * channels-last activations [n][d][h][w][c] in bf16, fp16 or fp32 whose
+ * pixels lie `pitch` elements apart (a channel slice of a wider tensor; the
+ * pixels themselves are consecutive). Units and groups as in
+ * conv3d_group_norm. With N the values of a unit and group, all in fp32 and
+ * rounded once, at the end (conv3d_group_norm also rounds before its SiLU):
+ *   mean = sum x / N, rstd = 1 / sqrt(sum (x - mean)^2 / N + eps)
+ *   h = (x - mean) * rstd, a = h * gamma[c] + beta[c]
+ *   y = a * sigmoid(a) with silu, else a
+ * and for the gradient dy of y
+ *   da = dy * (sigmoid(a) + a * sigmoid'(a)) with silu, else dy
+ *   c1 = sum over unit and group of gamma * da / N, c2 = of gamma * da * h / N
+ *   dx = rstd * (gamma * da - c1 - h * c2)
+ *   dgamma[c] = sum over all pixels of da * h, dbeta[c] = of da
+ * A NaN or an infinity makes its own unit and group (and in dgamma, dbeta its
+ * channels) NaN. Differences from the mean beyond 2^63 overflow the sum of
+ * squares. Results do not change from call to call (no atomics). */
+typedef enum { CONV3D_ELT_BF16 = 0, CONV3D_ELT_FP16 = 1, CONV3D_ELT_FP32 = 2 } conv3d_elt;
+
+typedef struct {
+  int n, d, h, w, c;   /* extents */
+  int groups;          /* c % groups == 0 */
+  int t_isolated;      /* 1: statistics per frame; 0: per sample */
+  int silu;            /* 1: SiLU after the affine */
+  float eps;           /* > 0, finite */
+  int dtype;           /* conv3d_elt of x, y, dy and dx */
+  long long x_pitch;   /* elements between pixels of x; 0: c */
+  long long y_pitch;   /* of y and dy; 0: c */
+  long long dx_pitch;  /* of dx; 0: c */
+} conv3d_group_norm_train_desc;
+
+/* Workspace bytes of the forward (backward = 0) or backward pass. */
+conv3d_status conv3d_group_norm_train_workspace_bytes(const conv3d_group_norm_train_desc* desc,
+                                                      int backward, size_t* bytes);
+
+/* y and stats from x.
+ *   gamma, beta  fp32 [c]
+ *   stats        fp32 [units][groups][2]: mean, rstd (written)
+ *   workspace    conv3d_group_norm_train_workspace_bytes(desc, 0), 16-byte aligned
+ * x and y are aligned to their type, the rest to 4 bytes; 16-byte aligned
+ * pixels are fastest. No two operands may overlap, but x and y may be
+ * different channels of one tensor.
+ * Errors: a size < 1, c % groups, eps not > 0, a pitch below c ->
+ * CONV3D_ERR_SHAPE; c > 65536, a tensor over 2^40 bytes, 2^24 or more units
+ * times groups -> CONV3D_ERR_UNSUPPORTED. */
+conv3d_status conv3d_group_norm_train_fwd(const conv3d_group_norm_train_desc* desc, const void* x,
+                                          const float* gamma, const float* beta, void* y,
+                                          float* stats, void* workspace, size_t workspace_bytes,
+                                          void* stream);
+
+/* dx, dgamma and dbeta (fp32 [c], overwritten) from dy, the forward pass's x
+ * and stats. Each of the three may be NULL (not wanted), but not all. dx may
+ * be dy itself (same pitch); no other overlap. Workspace:
+ * conv3d_group_norm_train_workspace_bytes(desc, 1). Other rules as above. */
+conv3d_status conv3d_group_norm_train_bwd(const conv3d_group_norm_train_desc* desc, const void* dy,
+                                          const void* x, const float* gamma, const float* beta,
+                                          const float* stats, void* dx, float* dgamma,
+                                          float* dbeta, void* workspace, size_t workspace_bytes,
+                                          void* stream);
+
+/* ------------------------------------- training: channel norm + SiLU, backward
+ * Backward pass of CONV3D_EPI_L2NORM_SILU (the fused epilogue and
+ * conv3d_norm_silu) for the gradient dy of its output. With `value` the
+ * pre-norm sum that CONV3D_EPI_RESIDUAL_OUT writes, den = max(|value|, 1e-12)
+ * over a pixel's channels, e = value * sqrt(c) / den, a = e * gamma:
+ *   da = dy * (sigmoid(a) + a * sigmoid'(a)), g = da * gamma * sqrt(c) / den
+ *   dvalue = B(g - value * (sum_c g * value) / |value|^2 + dskip)
+ *            (without the second term where |value| <= 1e-12)
+ *   dgamma[c] = sum over the pixels of da * e, dbias[c] = of dvalue before B
+ * in fp32, without the forward pass's intermediate roundings. dvalue is the
+ * gradient of the conv's output and of the residual; dskip (or NULL) is the
+ * gradient that reaches `value` past the norm, through residual_out.
+ *   value, dy, dskip, dvalue  bf16 NDHWC [n][d][h][w][c], gamma bf16 [c]
+ *   dgamma, dbias             fp32 [c], overwritten; each may be NULL
+ *   workspace                 conv3d_norm_silu_bwd_workspace_bytes; may be
+ *                             NULL when neither dgamma nor dbias is wanted
+ * c % 8 == 0, c <= 2048; dgamma and dbias 4-byte aligned, the rest 16-byte
+ * aligned. dvalue may be dy or dskip itself; no other overlap of an output. */
+conv3d_status conv3d_norm_silu_bwd_workspace_bytes(int n, int d, int h, int w, int c,
+                                                   size_t* bytes);
+conv3d_status conv3d_norm_silu_bwd(const void* value, const void* dy, const void* dskip, int n,
+                                   int d, int h, int w, int c, const void* gamma, void* dvalue,
+                                   float* dgamma, float* dbias, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------- training: gradient norm, clipping
+ * Over all elements of `count` gradient tensors:
+ *   norm = sqrt(sum g^2) (CONV3D_GRAD_NORM_L2; squares and sums in fp64) or
+ *          max |g| (CONV3D_GRAD_NORM_INF); a NaN makes it NaN
+ *   coef = min(1, max_norm / (norm + 1e-6)); a NaN norm gives NaN
+ *   out  = g * coef, in fp32, rounded once to out's type
+ * Tensors are dense, of any length (0 included) and aligned to their type.
+ * `out` may be `grad` or NULL (in place, out_dtype = dtype), or another
+ * tensor, of any of the types: gradients clipped into fp32 copies. Nothing is
+ * written in place where coef is 1. `grads` is host memory and is not read
+ * after the call returns; the addresses travel with the launches, so a
+ * captured call replays on them. */
+typedef struct {
+  void* grad;
+  void* out;           /* conv3d_grad_clip only */
+  long long numel;
+  int dtype;           /* conv3d_elt of grad */
+  int out_dtype;       /* conv3d_elt of out */
+} conv3d_grad;
+
+enum { CONV3D_GRAD_NORM_L2 = 0, CONV3D_GRAD_NORM_INF = 1 };
+
+/* Workspace bytes of both calls below (addresses in grads are not looked at). */
+conv3d_status conv3d_grad_workspace_bytes(const conv3d_grad* grads, int count, size_t* bytes);
+
+/* *norm (device, fp32) = the norm; nothing else is written. */
+conv3d_status conv3d_grad_norm(const conv3d_grad* grads, int count, int norm_type, float* norm,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* The norm (before clipping) to *norm, and the clipped gradients. max_norm is
+ * finite and not negative (CONV3D_ERR_SHAPE). What is written may overlap
+ * nothing else: the same tensor twice in place is CONV3D_ERR_OVERLAP. */
+conv3d_status conv3d_grad_clip(const conv3d_grad* grads, int count, int norm_type, float max_norm,
+                               float* norm, void* workspace, size_t workspace_bytes,
+                               void* stream);
 
 /* Human-readable name of a status code (static string). */
 const char* conv3d_status_str(conv3d_status status);
