@@ -50,27 +50,43 @@ __device__ __forceinline__ Pack<T, VEC> pack(const float (&f)[VEC]) {
   return p;
 }
 
-// The parts of the logistic function for a: with t = e^-|a| (<= 1, nothing
-// overflows) and q = 1 / (1 + t), sigmoid(a) is q for a >= 0 and t q below,
-// and its slope is t q^2. e^-|a| is 2^-(|a| log2 e); with EXACT the rounding
-// of that product is made good (fp32 results; below the rounding of 16-bit
-// ones). |a| is capped where t is zero anyway, so no infinity meets its
-// negative; a NaN goes through the callers' products with a.
+// e^-a / its logistic. 16-bit results: t = 2^(-a log2 e) by the hardware
+// exponential; it overflows to infinity below a = -88, where 1 / (1 + t) = 0 is
+// the rounded value anyway. fp32 results (EXACT): the rounding of a log2 e is
+// made good by a second product, and only e^-|a| is formed, so that 1 - sig
+// needs no difference. A NaN stays in both.
 template <bool EXACT>
-__device__ __forceinline__ void logistic(float a, float& sig, float& slope) {
+__device__ __forceinline__ float exp_neg(float v) {
   constexpr float kLog2e = 1.44269502162933349609375f;
+  if (!EXACT) return __builtin_amdgcn_exp2f(-v * kLog2e);
   constexpr float kLog2eLo = 1.925963033500011e-08f;   // log2(e) - kLog2e
   constexpr float kLn2 = 0.693147182464599609375f;
-  const float m = fminf(fabsf(a), 256.0f);
+  const float m = fminf(v, 256.0f);                    // t is 0 there, and no infinity meets 0
   const float p = m * kLog2e;
-  float t = __builtin_amdgcn_exp2f(-p);
-  if (EXACT) {
-    const float r = __builtin_fmaf(m, kLog2eLo, __builtin_fmaf(m, kLog2e, -p));
-    t = __builtin_fmaf(t, -r * kLn2, t);
-  }
+  const float t = __builtin_amdgcn_exp2f(-p);
+  const float r = __builtin_fmaf(m, kLog2eLo, __builtin_fmaf(m, kLog2e, -p));
+  return __builtin_fmaf(t, -r * kLn2, t);
+}
+
+// a sigmoid(a).
+template <bool EXACT>
+__device__ __forceinline__ float silu_of(float a) {
+  if (!EXACT) return a * __builtin_amdgcn_rcpf(1.0f + exp_neg<false>(a));
+  const float t = exp_neg<true>(fabsf(a));
   const float q = __builtin_amdgcn_rcpf(1.0f + t);
-  sig = a >= 0.0f ? q : t * q;
-  slope = t * q * q;
+  return a * (a >= 0.0f ? q : t * q);
+}
+
+// Its derivative sigmoid(a) (1 + a (1 - sigmoid(a))).
+template <bool EXACT>
+__device__ __forceinline__ float silu_slope(float a) {
+  if (!EXACT) {
+    const float sig = __builtin_amdgcn_rcpf(1.0f + exp_neg<false>(a));
+    return sig * __builtin_fmaf(a, 1.0f - sig, 1.0f);
+  }
+  const float t = exp_neg<true>(fabsf(a));
+  const float q = __builtin_amdgcn_rcpf(1.0f + t);
+  return __builtin_fmaf(a, t * q * q, a >= 0.0f ? q : t * q);
 }
 
 }  // namespace conv3d

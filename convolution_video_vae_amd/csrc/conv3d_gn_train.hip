@@ -244,11 +244,7 @@ __global__ __launch_bounds__(kThreads) void gn_train_apply_kernel(GnTrainArgs a,
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
           f[j] = fmaf(f[j] - mean[j], scale[j], beta[j]);
-          if (SILU) {
-            float sig, slope;
-            logistic<T::kWide>(f[j], sig, slope);
-            f[j] *= sig;
-          }
+          if (SILU) f[j] = silu_of<T::kWide>(f[j]);
         }
         *(Pack<T, VEC>*)(y + q * yp) = pack<T, VEC>(f);
       });
@@ -271,13 +267,7 @@ struct BwdLane {
   }
   __device__ __forceinline__ void value(int j, float x, float dy, float& h, float& da) const {
     h = (x - mean[j]) * rstd[j];
-    da = dy;
-    if (SILU) {
-      const float v = fmaf(h, gamma[j], beta[j]);
-      float sig, slope;
-      logistic<T::kWide>(v, sig, slope);
-      da = dy * fmaf(v, slope, sig);
-    }
+    da = SILU ? dy * silu_slope<T::kWide>(fmaf(h, gamma[j], beta[j])) : dy;
   }
 };
 
@@ -500,16 +490,15 @@ int run_bwd(const GnTrainArgs& a, const Rows& r, hipStream_t s) {
   return a.silu ? run_bwd_act<T, VEC, true>(a, r, s) : run_bwd_act<T, VEC, false>(a, r, s);
 }
 
-// The widest of 16-byte vectors, 4-byte ones and single elements that the
-// tensors allow (a 4-byte type has no step between).
+// The widest of 16-byte vectors, pairs and single elements that the tensors
+// allow.
 template <class T>
 int run(const GnTrainArgs& a, bool bwd, hipStream_t s) {
-  constexpr int wide = 16 / sizeof(typename T::store), mid = 4 / sizeof(typename T::store);
+  constexpr int wide = 16 / sizeof(typename T::store);
   Rows r;
   if (rows_for(a, wide, bwd, &r))
     return bwd ? run_bwd<T, wide>(a, r, s) : run_fwd<T, wide>(a, r, s);
-  if (mid > 1 && rows_for(a, mid, bwd, &r))
-    return bwd ? run_bwd<T, mid>(a, r, s) : run_fwd<T, mid>(a, r, s);
+  if (rows_for(a, 2, bwd, &r)) return bwd ? run_bwd<T, 2>(a, r, s) : run_fwd<T, 2>(a, r, s);
   rows_for(a, 1, bwd, &r);
   return bwd ? run_bwd<T, 1>(a, r, s) : run_fwd<T, 1>(a, r, s);
 }

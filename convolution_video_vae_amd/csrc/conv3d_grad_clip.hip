@@ -179,12 +179,15 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradBatch b) {
   if (b.norm && blockIdx.x == 0 && threadIdx.x == 0) *b.norm = (float)norm;
   const double c = (double)b.max_norm / (norm + 1e-6);
   const float coef = c > 1.0 ? 1.0f : (float)c;      // a NaN is not above 1
-  const int i = find_item(b, blockIdx.x);
+  // from the last block back: what the norm pass read last is still in the
+  // memory-side cache
+  const int block = gridDim.x - 1 - blockIdx.x;
+  const int i = find_item(b, block);
   const void* src = b.item[i].src;
   void* dst = b.item[i].dst;
   const int dtype = b.item[i].dtype, out = b.item[i].out_dtype;
   if (coef == 1.0f && src == dst) return;            // in place, and nothing changes
-  const long long at = (long long)((int)blockIdx.x - b.item[i].first) * b.chunk;
+  const long long at = (long long)(block - b.item[i].first) * b.chunk;
   const int n = (int)min((long long)b.chunk, b.item[i].numel - at);
   if (dtype == ELT_BF16) scale_to<Bf16>(src, dst, out, at, n, coef);
   else if (dtype == ELT_FP16) scale_to<Fp16>(src, dst, out, at, n, coef);

@@ -18,6 +18,7 @@
 #include <hip/hip_runtime.h>
 
 #include "conv3d_device.h"
+#include "conv3d_colsum.h"
 #include "conv3d_elt.h"
 #include "conv3d_train.h"
 
@@ -87,9 +88,7 @@ __global__ __launch_bounds__(kThreads) void ns_bwd_kernel(NsBwdArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float e = v[k][j] * s, act = e * gamma[k][j];
-        float sig, slope;
-        logistic<false>(act, sig, slope);
-        const float da = d[j] * fmaf(act, slope, sig);
+        const float da = d[j] * silu_slope<false>(act);
         if (SUMS) dg[k][j] = fmaf(da, e, dg[k][j]);
         g[k][j] = da * gamma[k][j];
         dot = fmaf(g[k][j], e, dot);
@@ -134,27 +133,6 @@ __global__ __launch_bounds__(kThreads) void ns_bwd_kernel(NsBwdArgs a) {
           out[which * a.C + c + kThreads] = t;
         }
       }
-  }
-}
-
-// dgamma and dbias from the work-groups' partial sums, in fp64 and work-group
-// order: 32 columns x 8 lanes of work-groups each.
-__global__ __launch_bounds__(kThreads) void ns_bwd_params_kernel(NsBwdArgs a) {
-  __shared__ double part[8][32];
-  const int cl = threadIdx.x & 31, bl = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + cl;      // of [dgamma C][dbias C]
-  double t = 0.0;
-  if (col < 2 * a.C)
-    for (int b = bl; b < a.blocks; b += 8) t += (double)a.partial[(long long)b * 2 * a.C + col];
-  part[bl][cl] = t;
-  __syncthreads();
-  if (bl == 0 && col < 2 * a.C) {
-    for (int i = 1; i < 8; ++i) t += part[i][cl];
-    if (col < a.C) {
-      if (a.dgamma) a.dgamma[col] = (float)t;
-    } else if (a.dbias) {
-      a.dbias[col - a.C] = (float)t;
-    }
   }
 }
 
@@ -205,7 +183,8 @@ int launch_ns_bwd(const NsBwdArgs& a, void* stream) {
   }
 #undef CONV3D_NS_CASE
   if (a.dgamma || a.dbias)
-    hipLaunchKernelGGL(ns_bwd_params_kernel, dim3((2 * a.C + 31) / 32), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL(column_sums_kernel, dim3((2 * a.C + kSumCols - 1) / kSumCols),
+                       dim3(kSumThreads), 0, s, a.partial, a.blocks, a.C, a.dgamma, a.dbias);
   return (int)hipGetLastError();
 }
 
