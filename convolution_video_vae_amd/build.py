@@ -35,8 +35,8 @@ def build(verbose: bool = False) -> str:
     units = [("conv3d_igemm", [f"-DCONV3D_PART={k}", f"-DCONV3D_NPARTS={IGEMM_PARTS}"],
               f"conv3d_igemm_{k}") for k in range(IGEMM_PARTS)]
     units += [("conv3d_kernels", [], "conv3d_kernels"), ("conv3d_norm", [], "conv3d_norm")]
-    units += [(name, [], name) for name in ("conv3d_gn_train", "conv3d_ns_bwd",
-                                            "conv3d_grad_clip")]
+    units += [(name, [], name) for name in ("conv3d_gn_train", "conv3d_gn_resident",
+                                            "conv3d_ns_bwd", "conv3d_grad_clip")]
     for name, defs, oname in units:
         obj = os.path.join(BUILD, oname + ".o")
         jobs.append([HIPCC, "-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC", "-c",

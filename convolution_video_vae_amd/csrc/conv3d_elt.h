@@ -50,7 +50,47 @@ __device__ __forceinline__ Pack<T, VEC> pack(const float (&f)[VEC]) {
   return p;
 }
 
-// e^-a / its logistic. 16-bit results: t = 2^(-a log2 e) by the hardware
+// 16 bytes of elements as they are kept in registers, four of them: the
+// compiler would give every 16-bit element of a Pack a register of its own.
+template <class T>
+struct Held {
+  static constexpr int VEC = 16 / sizeof(typename T::store);
+  u32x4_t v;
+  __device__ __forceinline__ void get(float (&f)[VEC]) const {
+    if constexpr (VEC == 4) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = __builtin_bit_cast(float, (unsigned)v[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[2 * j] = T::get((typename T::store)(v[j] & 0xffffu));
+        f[2 * j + 1] = T::get((typename T::store)(v[j] >> 16));
+      }
+    }
+  }
+  __device__ __forceinline__ void put(const float (&f)[VEC]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (VEC == 4) v[j] = __builtin_bit_cast(unsigned, f[j]);
+      else v[j] = (unsigned)T::put(f[2 * j]) | ((unsigned)T::put(f[2 * j + 1]) << 16);
+    }
+  }
+};
+template <>
+__device__ __forceinline__ void Held<Bf16>::get(float (&f)[8]) const {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = bf_lo(v[j]);
+    f[2 * j + 1] = bf_hi(v[j]);
+  }
+}
+template <>
+__device__ __forceinline__ void Held<Bf16>::put(const float (&f)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = pack2(f[2 * j], f[2 * j + 1]);
+}
+
+// e^-a. 16-bit results: t = 2^(-a log2 e) by the hardware
 // exponential; it overflows to infinity below a = -88, where 1 / (1 + t) = 0 is
 // the rounded value anyway. fp32 results (EXACT): the rounding of a log2 e is
 // made good by a second product, and only e^-|a| is formed, so that 1 - sig

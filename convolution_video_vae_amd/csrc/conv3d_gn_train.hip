@@ -36,6 +36,7 @@
 
 #include "conv3d_device.h"
 #include "conv3d_elt.h"
+#include "conv3d_gn_device.h"
 #include "conv3d_train.h"
 
 namespace conv3d {
@@ -166,12 +167,6 @@ __global__ __launch_bounds__(kThreads) void gn_train_stats_kernel(GnTrainArgs a,
     }
   }
   join_channels<VEC>(a, r, l, t1, t2, a.partial + (long long)blockIdx.x * a.C * 2);
-}
-
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
-  return v;
 }
 
 // Sums two values over the work-group, in lane and wave order.
@@ -347,17 +342,6 @@ __global__ __launch_bounds__(kThreads) void gn_train_bwd_finalize_kernel(GnTrain
     a.coef[(long long)blockIdx.x * 2] = (float)(d1 / N);
     a.coef[(long long)blockIdx.x * 2 + 1] = (float)(d2 / N);
   }
-}
-
-// rstd (gamma da - c1 - h c2), each product rounded on its own: the three
-// terms cancel where a group holds few values, and to exactly zero where it
-// holds one.
-__device__ __forceinline__ float gn_dx(float rstd, float gamma, float da, float c1, float h,
-                                       float c2) {
-#pragma clang fp contract(off)
-  const float t = gamma * da;
-  const float s = h * c2;
-  return rstd * (t - c1 - s);
 }
 
 template <class T, int VEC, bool SILU>

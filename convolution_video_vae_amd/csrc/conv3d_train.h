@@ -39,6 +39,23 @@ struct GnTrainArgs {
 int launch_gn_train_fwd(const GnTrainArgs& args, void* stream);
 int launch_gn_train_bwd(const GnTrainArgs& args, void* stream);
 
+// The same with the activations read once (conv3d_gn_resident.hip): each
+// work-group keeps a piece of a unit in registers. A range is Gb whole groups
+// (Cb channels in Vb 16-byte vectors), NR of them make C; the unit's pixels
+// are cut into W pieces of piece_px = ppi * passes.
+constexpr int kGnResThreadsFwd = 512, kGnResThreadsBwd = 256;
+constexpr int kGnResRows = 16;                         // rows a thread can hold
+constexpr int kGnResWords = 2048;                      // words of one exchange
+struct GnResPlan {
+  int Cb, Vb, NR, Gb;
+  int ppi, passes, piece_px, W;
+  int parts;                 // lanes of rows that join a channel's sums
+  int spin;                  // polls of one word before a work-group helps itself
+  unsigned long long* words; // [units][NR][W][Gb] (W > 1)
+  float* channel_sums;       // backward: [units][W][2][C], or null
+};
+int launch_gn_resident(const GnTrainArgs& args, const GnResPlan& plan, bool bwd, void* stream);
+
 // Backward pass of the channel L2 norm x sqrt(C) x gamma -> SiLU
 // (conv3d_ns_bwd.hip) over M rows of C channels.
 struct NsBwdArgs {

@@ -28,7 +28,63 @@ constexpr long long kGnMinChunk = 64;                // pixels; a chunk leaves 1
 struct GnTrainPlan {
   GnTrainArgs a;
   size_t off_chan, off_coef, total;
+  bool fits;                 // r: the activations may stay in registers
+  GnResPlan r;
+  size_t off_sums;
 };
+
+constexpr int kGnMaxPieces = 128;        // of one exchange; 512 work-groups are resident
+constexpr int kGnFill = 512;             // work-groups that fill the chip
+constexpr int kGnSpin = 20000;           // polls (about a microsecond each) before helping oneself
+
+int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
+
+// Ranges and pieces of the resident form for 16-byte vectors; false where a
+// unit's pieces are too many to be on the chip together.
+bool plan_resident(const GnTrainArgs& a, bool bwd, GnResPlan* r) {
+  const int size = elt_size(a.dtype), vec = 16 / size;
+  const int rows = kGnResRows, threads = bwd ? kGnResThreadsBwd : kGnResThreadsFwd;
+  if (a.C % vec) return false;
+  const int quantum = a.cpg / gcd(a.cpg, vec) * vec;    // whole groups in whole vectors
+  const auto lay = [&](int Cb) {
+    r->Cb = Cb;
+    r->Vb = Cb / vec;
+    r->NR = a.C / Cb;
+    r->Gb = Cb / a.cpg;
+    r->ppi = threads / r->Vb;
+    r->parts = std::min(threads / Cb, r->ppi);
+  };
+  const int limit = std::min(a.C, threads);
+  // one work-group per range: the narrowest range of at least 64 bytes a pixel
+  for (int Cb = quantum; Cb <= limit; Cb += quantum) {
+    if (a.C % Cb || (Cb * size < 64 && Cb < a.C)) continue;
+    lay(Cb);
+    r->passes = (int)std::min((a.P + r->ppi - 1) / r->ppi, (long long)rows + 1);
+    if (r->passes <= rows) {
+      r->W = 1;
+      r->piece_px = r->ppi * r->passes;
+      return (long long)a.units * r->NR <= kGnMaxItems / 2;   // 512 threads each
+    }
+    break;
+  }
+  // pieces: whole 128-byte lines, as few pieces as hold the unit, but enough
+  // work-groups to fill the chip
+  for (int Cb = quantum; Cb <= limit; Cb += quantum) {
+    if (a.C % Cb || (Cb * size < 128 && Cb < a.C)) continue;
+    lay(Cb);
+    const long long lanes = (a.P + r->ppi - 1) / r->ppi;        // rows per thread in all
+    const long long fill = (kGnFill + (long long)a.units * r->NR - 1) / ((long long)a.units * r->NR);
+    long long W = std::max((lanes + rows - 1) / rows, std::min(fill, (lanes + 1) / 2));
+    if ((lanes + rows - 1) / rows > kGnMaxPieces) return false;
+    W = std::min(W, (long long)kGnMaxPieces);
+    r->passes = (int)((lanes + W - 1) / W);
+    r->piece_px = r->ppi * r->passes;
+    r->W = (int)((a.P + r->piece_px - 1) / r->piece_px);
+    return r->W * r->Gb <= kGnResWords && (long long)a.units * r->NR * r->W <= kGnMaxItems / 2 &&
+           (long long)a.units * r->NR * r->W * r->Gb <= (1LL << 30);
+  }
+  return false;
+}
 
 conv3d_status plan_gn_train(const conv3d_group_norm_train_desc* d, bool bwd, GnTrainPlan* pl) {
   if (!d) return CONV3D_ERR_NULL;
@@ -76,7 +132,23 @@ conv3d_status plan_gn_train(const conv3d_group_norm_train_desc* d, bool bwd, GnT
     at += (size_t)units * a.G * 8;
   }
   pl->total = (at + 255) / 256 * 256;
+  // the resident form needs its words and channel sums instead
+  pl->r = GnResPlan{};
+  pl->r.spin = kGnSpin;
+  pl->fits = plan_resident(a, bwd, &pl->r);
+  if (pl->fits) {
+    const GnResPlan& r = pl->r;
+    at = r.W > 1 ? (size_t)units * r.NR * r.W * r.Gb * 8 : 0;
+    pl->off_sums = at = (at + 255) / 256 * 256;
+    if (bwd) at += (size_t)units * r.W * 2 * a.C * 4;
+    pl->total = std::max(pl->total, (at + 255) / 256 * 256);
+  }
   return CONV3D_OK;
+}
+
+// Whether an operand's pixels are 16-byte vectors.
+bool vectors(const void* p, long long pitch, int size) {
+  return aligned16(p) && (pitch * size) % 16 == 0;
 }
 
 // One operand: `pixels` rows of `c` elements at a pitch.
@@ -144,6 +216,10 @@ conv3d_status conv3d_group_norm_train_fwd(const conv3d_group_norm_train_desc* de
   a.gamma = gamma;
   a.beta = beta;
   a.stats = stats;
+  if (pl.fits && vectors(x, a.x_pitch, size) && vectors(y, a.out_pitch, size)) {
+    pl.r.words = (unsigned long long*)workspace;
+    return launch_gn_resident(a, pl.r, false, stream) ? CONV3D_ERR_HIP : CONV3D_OK;
+  }
   a.partial = (double*)workspace;
   return launch_gn_train_fwd(a, stream) ? CONV3D_ERR_HIP : CONV3D_OK;
 }
@@ -179,9 +255,10 @@ conv3d_status conv3d_group_norm_train_bwd(const conv3d_group_norm_train_desc* de
     for (int j = 0; j < i; ++j)
       if (overlaps(small[i], small[j])) return CONV3D_ERR_OVERLAP;
   }
+  bool in_place = false;
   if (dx) {
     const Pitched po = pitched(dx, pixels, a.C, a.out_pitch, size);
-    const bool in_place = dx == dy && a.out_pitch == a.dy_pitch;
+    in_place = dx == dy && a.out_pitch == a.dy_pitch;
     if (share(po, px) || (!in_place && share(po, pd))) return CONV3D_ERR_OVERLAP;
     for (const Range& r : small)
       if (overlaps(po.r, r)) return CONV3D_ERR_OVERLAP;
@@ -199,6 +276,15 @@ conv3d_status conv3d_group_norm_train_bwd(const conv3d_group_norm_train_desc* de
   a.coef = (float*)((char*)workspace + pl.off_coef);
   a.dgamma = dgamma;
   a.dbeta = dbeta;
+  // in place, a work-group that has to form another piece's sums itself would
+  // read what that piece's own work-group may have overwritten
+  if (pl.fits && !(in_place && pl.r.W > 1) && vectors(x, a.x_pitch, size) &&
+      vectors(dy, a.dy_pitch, size) && (!dx || vectors(dx, a.out_pitch, size))) {
+    pl.r.words = (unsigned long long*)workspace;
+    pl.r.channel_sums =
+        dgamma || dbeta ? (float*)((char*)workspace + pl.off_sums) : nullptr;
+    return launch_gn_resident(a, pl.r, true, stream) ? CONV3D_ERR_HIP : CONV3D_OK;
+  }
   return launch_gn_train_bwd(a, stream) ? CONV3D_ERR_HIP : CONV3D_OK;
 }
 
