@@ -88,71 +88,162 @@ __device__ __forceinline__ int rows_of(const GnTrainArgs& a, const GnResPlan& r,
   return h.active && *first < p1 ? (int)((p1 - *first + r.ppi - 1) / r.ppi) : 0;
 }
 
-template <class T, int R>
-__device__ __forceinline__ void load_rows(const void* base, long long pitch, long long at,
-                                          int channel0, long long first, int ppi, int n,
-                                          Held<T> (&v)[R]) {
-  const typename T::store* p = (const typename T::store*)base + (at + first) * pitch + channel0;
-  const long long step = ppi * pitch;
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    if (i < n) v[i].v = *(const u32x4_t*)p;
-    p += step;
+// Group of element j of a thread's vector whose first channel (of the range)
+// is c: one division, then counting.
+struct GroupOf {
+  int g, left;
+  __device__ __forceinline__ GroupOf(int c, int cpg) : g(c / cpg), left(cpg - (c - c / cpg * cpg)) {}
+  __device__ __forceinline__ int next(int cpg) {
+    const int now = g;
+    if (--left == 0) {
+      ++g;
+      left = cpg;
+    }
+    return now;
   }
+};
+
+__device__ __forceinline__ double lanes_sum(double v, int lanes) {
+  for (int m = lanes >> 1; m > 0; m >>= 1) v += __shfl_xor(v, m);
+  return v;
 }
 
-// f(row) for the thread's n rows: the held ones, or (a work-group that helps
-// itself) those of another piece, read from memory one at a time.
-template <class T, int R, class F>
-__device__ __forceinline__ void held_rows(const Held<T> (&v)[R], int n, F f) {
-#pragma unroll
-  for (int i = 0; i < R; ++i)
-    if (i < n) f(v[i]);
-}
-template <class T, class F>
-__device__ __forceinline__ void memory_rows(const typename T::store* p, long long step, int n, F f) {
-#pragma unroll 1
-  for (int i = 0; i < n; ++i, p += step) {
-    Held<T> v;
-    v.v = *(const u32x4_t*)p;
-    f(v);
-  }
-}
+// ---- joining a work-group's rows
+//
+// Where a row's vectors are a power of two of lanes, rows of one wave are
+// joined by exchanges between lanes and only one value per wave goes through
+// LDS; else every lane's goes. Either way in a fixed order.
 
-// Channel sums of N quantities over the work-group's rows: s[k][j] of every
-// thread -> tot[k][channel of the range]. Rows are joined in a fixed order.
+// Channel sums of N quantities: s[k][j] of every thread -> tot[k][channel].
 template <int NT, int N, int VEC>
 struct ChannelSums {
   float red[N][NT * VEC];
-  float red2[N][NT];
   float tot[N][NT];
-  __device__ __forceinline__ void join(const GnResPlan& r, bool active, const float (&s)[N][VEC]) {
+  __device__ __forceinline__ void join(const GnResPlan& r, bool active, float (&s)[N][VEC]) {
     const int t = threadIdx.x;
-    __syncthreads();                       // the last user of these arrays is done
-    if (active) {
+    if (r.lanes) {
+      for (int m = r.Vb; m < 64; m <<= 1)
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) s[k][j] += __shfl_xor(s[k][j], m);
+    }
+    const int rows = r.lanes ? NT / 64 : r.ppi;
+    const int at = r.lanes ? (t >> 6) * r.Cb + (t & 63) * VEC : t * VEC;
+    if (r.lanes ? (t & 63) < r.Vb : active) {
 #pragma unroll
       for (int k = 0; k < N; ++k)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) red[k][t * VEC + j] = s[k][j];
-    }
-    __syncthreads();
-    const int part = t / r.Cb, col = t - part * r.Cb;
-    if (part < r.parts) {
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        float v = 0.0f;
-        for (int row = part; row < r.ppi; row += r.parts) v += red[k][row * r.Cb + col];
-        red2[k][t] = v;
-      }
+        for (int j = 0; j < VEC; ++j) red[k][at + j] = s[k][j];
     }
     __syncthreads();
     if (t < r.Cb) {
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        float v = red2[k][t];
-        for (int i = 1; i < r.parts; ++i) v += red2[k][i * r.Cb + t];
+        float v = red[k][t];
+        for (int i = 1; i < rows; ++i) v += red[k][i * r.Cb + t];
         tot[k][t] = v;
       }
+    }
+    __syncthreads();
+  }
+};
+
+// A sample of n values: their mean and the squares' sum about it. Two are
+// joined by Chan, Golub and LeVeque's update; nothing cancels.
+struct Moments {
+  float mean, m2;
+  __device__ __forceinline__ void join(float n, const Moments& o, float on) {
+    const float total = n + on;
+    const float d = o.mean - mean;
+    const float share = total > 0.0f ? on * __builtin_amdgcn_rcpf(total) : 0.0f;
+    m2 = m2 + o.m2 + d * d * (n * share);
+    mean = fmaf(d, share, mean);
+  }
+};
+
+// (mean, squares about it) of the groups of a piece to use(g, mean, m2), from
+// one Moments per slot (`fold` channels of one group) and wave (or lane row).
+template <int NT, int VEC>
+struct GroupMoments {
+  float mean[NT * VEC], m2[NT * VEC];
+  float n[NT];
+  template <class Use>
+  __device__ __forceinline__ void join(const GnResPlan& r, int cpg, bool active, int rows,
+                                       Moments (&s)[VEC], Use use) {
+    const int t = threadIdx.x;
+    float cnt = (float)rows;
+    // channels of one group in the vector: equal counts
+#pragma unroll
+    for (int f = 1; f < VEC; f *= 2)
+      if (r.fold > f) {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 2 * f) {
+          const float d = s[j + f].mean - s[j].mean;
+          s[j].m2 = s[j].m2 + s[j + f].m2 + d * d * (0.5f * cnt);
+          s[j].mean = fmaf(0.5f, d, s[j].mean);
+        }
+        cnt *= 2.0f;
+      }
+    if (r.lanes) {
+      for (int m = r.Vb; m < 64; m <<= 1) {
+        const float on = __shfl_xor(cnt, m);
+        const bool low = (t & m) == 0;          // both lanes join in the same order
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          if (j & (r.fold - 1)) continue;
+          Moments o;
+          o.mean = __shfl_xor(s[j].mean, m);
+          o.m2 = __shfl_xor(s[j].m2, m);
+          Moments a = low ? s[j] : o;
+          const Moments b = low ? o : s[j];
+          a.join(low ? cnt : on, b, low ? on : cnt);
+          s[j] = a;
+        }
+        cnt += on;
+      }
+    }
+    const int nrow = r.lanes ? NT / 64 : r.ppi;
+    const int slots = VEC / r.fold;             // of a thread's vector
+    const int width = r.Vb * slots;
+    const int lane = r.lanes ? t & 63 : t % r.Vb, row = r.lanes ? t >> 6 : t / r.Vb;
+    if (r.lanes ? lane < r.Vb : active) {
+      n[row * r.Vb + lane] = cnt;
+      int at = row * width + lane * slots;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        if (j & (r.fold - 1)) continue;
+        mean[at] = s[j].mean;
+        m2[at] = s[j].m2;
+        ++at;
+      }
+    }
+    __syncthreads();
+    // a group's entries (of its slots and the rows) over a few lanes, and those
+    const int per = cpg / r.fold, lg = r.entry_lanes, sub = t & (lg - 1);
+    for (int g = t / lg; g < r.Gb; g += NT / lg) {
+      Moments q = {0.0f, 0.0f};
+      float qn = 0.0f;
+      int i = sub / per, k = sub - i * per;
+      for (int e = sub; e < nrow * per; e += lg) {
+        const int slot = g * per + k;
+        const float on = n[i * r.Vb + slot / slots];
+        q.join(qn, Moments{mean[i * width + slot], m2[i * width + slot]}, on);
+        qn += on;
+        for (k += lg; k >= per; k -= per) ++i;
+      }
+      for (int m = lg >> 1; m > 0; m >>= 1) {
+        Moments o;
+        o.mean = __shfl_xor(q.mean, m);
+        o.m2 = __shfl_xor(q.m2, m);
+        const float on = __shfl_xor(qn, m);
+        const bool low = (sub & m) == 0;
+        Moments a = low ? q : o;
+        a.join(low ? qn : on, low ? o : q, low ? on : qn);
+        q = a;
+        qn += on;
+      }
+      if (sub == 0) use(g, q.mean, q.m2);
     }
     __syncthreads();
   }
@@ -180,40 +271,80 @@ __device__ __forceinline__ void each_group(int Gb, int cpg, Value value, Use use
   }
 }
 
-// The words of every piece of the (unit, range) into LDS; false where one
-// stayed empty.
+// ---- the exchange
+
+// Publishes this piece's words, which LDS holds, and adds those of the other
+// pieces of the (unit, range); false where one stayed empty.
 template <int NT>
-__device__ __forceinline__ bool gather(const unsigned long long* words, int n, int spin,
-                                       unsigned long long* xw, int* late) {
-  for (int i = threadIdx.x; i < n; i += NT) {
-    unsigned long long v = kEmpty;
-    for (int k = 0; k < spin; ++k) {
-      v = __hip_atomic_load(words + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      if (v != kEmpty) break;
-      __builtin_amdgcn_s_sleep(1);
+__device__ __forceinline__ bool exchange(const GnResPlan& r, const Where& h,
+                                         unsigned long long* xw, int* late) {
+  unsigned long long* words = r.words + ((long long)h.u * r.NR + h.range) * r.W * r.Gb;
+  const int own = h.w * r.Gb, n = r.W * r.Gb;
+  for (int i = own + threadIdx.x; i < own + r.Gb; i += NT)
+    __hip_atomic_store(words + i, xw[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  // four words in flight per thread: a poll is a trip to memory
+  for (int i0 = threadIdx.x; i0 < n; i0 += 4 * NT) {
+    unsigned long long v[4];
+    bool open[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = i0 + q * NT;
+      open[q] = i < n && !(i >= own && i < own + r.Gb);
+      v[q] = kEmpty;
     }
-    xw[i] = v;
-    if (v == kEmpty) *late = 1;
+    for (int k = 0; k < r.spin; ++k) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (open[q])
+          v[q] = __hip_atomic_load(words + i0 + q * NT, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      bool wait = false;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (open[q] && v[q] != kEmpty) {
+          xw[i0 + q * NT] = v[q];
+          open[q] = false;
+        }
+        wait |= open[q];
+      }
+      if (!wait) break;
+    }
+    if (open[0] | open[1] | open[2] | open[3]) *late = 1;
   }
   __syncthreads();
   return *late == 0;
 }
 
-__device__ __forceinline__ double piece_pixels(const GnTrainArgs& a, const GnResPlan& r, int w) {
-  const long long p0 = (long long)w * r.piece_px;
-  return (double)(min(a.P, p0 + r.piece_px) - p0);
+// f(g, lane) -> two sums over the pieces of group g, in fp64: as many lanes
+// per group (a power of two, at most a wave) as the work-group has.
+template <int NT, class F, class Use>
+__device__ __forceinline__ void over_pieces(const GnResPlan& r, F f, Use use) {
+  const int lg = r.join_lanes;
+  const int lane = threadIdx.x & (lg - 1);
+  for (int g = threadIdx.x / lg; g < r.Gb; g += NT / lg) use(g, lane, f(g, lane, lg));
 }
+// Steps of a vector's values are kept apart from each other: the compiler
+// would chain one value's exponential and reciprocal after another's to save
+// registers, and wait for each (two waves per SIMD hide nothing: 7.5 us of a
+// piece's 23).
+__device__ __forceinline__ void step_edge() { __builtin_amdgcn_sched_barrier(0); }
 
 template <class T, bool SILU, int R>
-__global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(GnTrainArgs a, GnResPlan r) {
+__global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(GnTrainArgs a,
+                                                                              GnResPlan r) {
   typedef typename T::store E;
-  constexpr int VEC = 16 / sizeof(E);
-  constexpr int NT = kGnResThreadsFwd;
-  __shared__ ChannelSums<NT, 1, VEC> sums;
+  constexpr int VEC = 16 / sizeof(E), NT = kGnResThreadsFwd;
+  __shared__ GroupMoments<NT, VEC> sums;
   __shared__ unsigned long long xw[kGnResWords];
   __shared__ float gmean[NT], grstd[NT];
+  __shared__ float lgamma[NT], lbeta[NT];
   __shared__ int late;
   const Where h = where(r);
+  // ahead of the rows: a load that is issued later returns after all of them,
+  // and after those of the other work-group on this CU
+  if (threadIdx.x < r.Cb) {
+    lgamma[threadIdx.x] = a.gamma[h.range * r.Cb + threadIdx.x];
+    lbeta[threadIdx.x] = a.beta[h.range * r.Cb + threadIdx.x];
+  }
   const int c0 = h.range * r.Cb + h.cv * VEC, gl0 = h.cv * VEC;
   const long long at = (long long)h.u * a.P;
   long long first;
@@ -221,82 +352,97 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
   Held<T> v[R];
   if (threadIdx.x == 0) late = 0;
 
-  // (mean, sum of squares about it) of a piece's groups, as words; rows(f)
-  // visits the thread's rows of the piece
-  const auto piece = [&](int w, unsigned long long* out, auto rows) {
-    const double px = piece_pixels(a, r, w) * a.cpg;
-    float s[1][VEC];
+  // Per channel, sums about the thread's first value (no cancellation where
+  // the mean is far above the spread) -> the piece's group moments as words.
+  // rows(f) visits the thread's rows of the piece.
+  const auto piece = [&](unsigned long long* out, int n, const Held<T>& v0, auto rows) {
+    float sh[VEC], s1[VEC], s2[VEC];
+    v0.get(sh);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) s[0][j] = 0.0f;
-    rows([&](const Held<T>& row) {
-      float f[VEC];
-      row.get(f);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) s[0][j] += f[j];
-    });
-    sums.join(r, h.active, s);
-    each_group<NT>(r.Gb, a.cpg, [&](int c) { return sums.tot[0][c]; },
-               [&](int g, float t) { gmean[g] = (float)((double)t / px); });
-    __syncthreads();
-    float m[VEC];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      m[j] = h.active ? gmean[(gl0 + j) / a.cpg] : 0.0f;
-      s[0][j] = 0.0f;
-    }
+    for (int j = 0; j < VEC; ++j) s1[j] = s2[j] = 0.0f;
     rows([&](const Held<T>& row) {
       float f[VEC];
       row.get(f);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        const float d = f[j] - m[j];
-        s[0][j] = fmaf(d, d, s[0][j]);
+        const float d = f[j] - sh[j];
+        s1[j] += d;
+        s2[j] = fmaf(d, d, s2[j]);
       }
     });
-    sums.join(r, h.active, s);
-    each_group<NT>(r.Gb, a.cpg, [&](int c) { return sums.tot[0][c]; },
-               [&](int g, float t) { out[g] = word_of(gmean[g], t); });
-    __syncthreads();
+    Moments m[VEC];
+    const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const float d = s1[j] * inv;
+      m[j].mean = n > 0 ? sh[j] + d : 0.0f;
+      m[j].m2 = fmaf(-d, s1[j], s2[j]);
+      m[j].m2 = m[j].m2 < 0.0f ? 0.0f : m[j].m2;      // and not fmaxf: a NaN stays
+    }
+    sums.join(r, a.cpg, h.active, n, m, [&](int g, float mu, float q) { out[g] = word_of(mu, q); });
   };
 
-  load_rows<T, R>(a.x, a.x_pitch, at, c0, first, r.ppi, n, v);
-  piece(h.w, xw + h.w * r.Gb, [&](auto f) { held_rows<T, R>(v, n, f); });
+  {
+    const E* p = (const E*)a.x + (at + first) * a.x_pitch + c0;
+    const long long step = r.ppi * a.x_pitch;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      v[i].v = u32x4_t{0, 0, 0, 0};
+      if (i < n) v[i].v = *(const u32x4_t*)p;
+      p += step;
+    }
+  }
+  piece(xw + h.w * r.Gb, n, v[0], [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (i < n) f(v[i]);
+  });
   if (r.W > 1) {
-    unsigned long long* words =
-        r.words + ((long long)h.u * r.NR + h.range) * r.W * r.Gb;
-    for (int g = threadIdx.x; g < r.Gb; g += NT)
-      __hip_atomic_store(words + h.w * r.Gb + g, xw[h.w * r.Gb + g], __ATOMIC_RELAXED,
-                         __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    if (!gather<NT>(words, r.W * r.Gb, r.spin, xw, &late)) {
+    if (!exchange<NT>(r, h, xw, &late)) {
       for (int w = 0; w < r.W; ++w) {
         long long fw;
         const int nw = rows_of(a, r, h, w, &fw);
         const E* p = (const E*)a.x + (at + fw) * a.x_pitch + c0;
-        piece(w, xw + w * r.Gb,
-              [&](auto f) { memory_rows<T>(p, r.ppi * a.x_pitch, nw, f); });
+        const long long step = r.ppi * a.x_pitch;
+        Held<T> v0;
+        v0.v = u32x4_t{0, 0, 0, 0};
+        if (nw > 0) v0.v = *(const u32x4_t*)p;
+        piece(xw + w * r.Gb, nw, v0, [&](auto f) {
+#pragma unroll 1
+          for (int i = 0; i < nw; ++i) {
+            Held<T> row;
+            row.v = *(const u32x4_t*)(p + i * step);
+            f(row);
+          }
+        });
       }
     }
   }
-  // pieces joined in fp64: a wave per group
-  for (int g = threadIdx.x >> 6; g < r.Gb; g += NT / 64) {
-    const int lane = threadIdx.x & 63;
-    const double N = (double)a.P * a.cpg;
-    double s = 0.0;
-    for (int w = lane; w < r.W; w += 64)
-      s += piece_pixels(a, r, w) * a.cpg * (double)word_lo(xw[w * r.Gb + g]);
-    const double mean = wave_sum(s) / N;
-    s = 0.0;
-    for (int w = lane; w < r.W; w += 64) {
-      const double d = (double)word_lo(xw[w * r.Gb + g]) - mean;
-      s += (double)word_hi(xw[w * r.Gb + g]) + piece_pixels(a, r, w) * a.cpg * d * d;
-    }
-    const double var = wave_sum(s) / N;
-    if (lane == 0) {
-      gmean[g] = (float)mean;
-      grstd[g] = (float)(1.0 / sqrt(var + (double)a.eps));
-    }
-  }
+  const double full = (double)r.piece_px * a.cpg;
+  const double last = (double)(a.P - (long long)(r.W - 1) * r.piece_px) * a.cpg;
+  const double inv_n = 1.0 / ((double)a.P * a.cpg);
+  over_pieces<NT>(
+      r,
+      [&](int g, int lane, int lg) {
+        // about the first piece's mean, so both sums are formed at once
+        const double k = (double)word_lo(xw[g]);
+        double s1 = 0.0, s2 = 0.0;
+        for (int w = lane; w < r.W; w += lg) {
+          const unsigned long long x = xw[w * r.Gb + g];
+          const double d = (double)word_lo(x) - k, nd = (w == r.W - 1 ? last : full) * d;
+          s1 += nd;
+          s2 += (double)word_hi(x) + nd * d;
+        }
+        s1 = lanes_sum(s1, lg) * inv_n;
+        const double var = lanes_sum(s2, lg) * inv_n - s1 * s1;
+        return double2{k + s1, var < 0.0 ? 0.0 : var};        // and not fmax: a NaN stays
+      },
+      [&](int g, int lane, double2 mv) {
+        if (lane == 0) {
+          gmean[g] = (float)mv.x;
+          grstd[g] = (float)(1.0 / sqrt(mv.y + (double)a.eps));
+        }
+      });
   __syncthreads();
   if (h.w == 0) {
     float* st = a.stats + ((long long)h.u * a.G + h.range * r.Gb) * 2;
@@ -306,26 +452,43 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
     }
   }
   if (!h.active) return;
+  // 16-bit types: one product per value, x scale + (beta - mean scale); its
+  // roundings are 2^-24 of x's own, x holds 8 or 11 bits. fp32: the
+  // difference from the mean first.
   float mean[VEC], scale[VEC], beta[VEC];
+  GroupOf go(gl0, a.cpg);
 #pragma unroll
   for (int j = 0; j < VEC; ++j) {
-    const int g = (gl0 + j) / a.cpg;
+    const int g = go.next(a.cpg);
     mean[j] = gmean[g];
-    scale[j] = grstd[g] * a.gamma[c0 + j];
-    beta[j] = a.beta[c0 + j];
+    scale[j] = grstd[g] * lgamma[gl0 + j];
+    beta[j] = lbeta[gl0 + j];
+    if (!T::kWide) beta[j] = fmaf(-mean[j], scale[j], beta[j]);
   }
   E* y = (E*)a.out + (at + first) * a.out_pitch + c0;
   const long long step = r.ppi * a.out_pitch;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    __builtin_amdgcn_sched_barrier(0);
     if (i < n) {
       float f[VEC];
       v[i].get(f);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        f[j] = fmaf(f[j] - mean[j], scale[j], beta[j]);
-        if (SILU) f[j] = silu_of<T::kWide>(f[j]);
+        f[j] = fmaf(T::kWide ? f[j] - mean[j] : f[j], scale[j], beta[j]);
+        if (SILU && T::kWide) f[j] = silu_of<true>(f[j]);
+      }
+      if (SILU && !T::kWide) {
+        constexpr float kLog2e = 1.44269502162933349609375f;
+        float t[VEC];
+        step_edge();
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) t[j] = __builtin_amdgcn_exp2f(-f[j] * kLog2e);
+        step_edge();
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) t[j] = __builtin_amdgcn_rcpf(1.0f + t[j]);
+        step_edge();
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) f[j] *= t[j];
       }
       Held<T> o;
       o.put(f);
@@ -335,14 +498,71 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
   }
 }
 
-template <class T, bool SILU, int R>
-__global__ __launch_bounds__(kGnResThreadsBwd, 2) void gn_resident_bwd_kernel(GnTrainArgs a, GnResPlan r) {
+// h and da of a vector from its channels' constants. 16-bit types: h =
+// x rstd - mean rstd in one product, a sigmoid's argument straight in powers
+// of two (p = -a log2 e), and 1 + a (1 - sigmoid) from p. fp32: as the
+// formulas say.
+template <class T, bool SILU, int VEC, int GV>
+struct BwdValues {
+  float mean[GV], rstd[GV], gamma[VEC], beta[VEC];
+  static constexpr int at(int j) { return j * GV / VEC; }
+  __device__ __forceinline__ void init(int j, float m, float s, float g, float b) {
+    constexpr float kLog2e = 1.44269502162933349609375f;
+    mean[at(j)] = T::kWide ? m : -m * s;
+    rstd[at(j)] = s;
+    gamma[j] = T::kWide ? g : -g * kLog2e;
+    beta[j] = T::kWide ? b : -b * kLog2e;
+  }
+  __device__ __forceinline__ float h(int j, float x) const {
+    return T::kWide ? mul_alone(x - mean[at(j)], rstd[at(j)])
+                    : fmaf(x, rstd[at(j)], mean[at(j)]);
+  }
+  // x becomes h, dy becomes da
+  __device__ __forceinline__ void run(float (&x)[VEC], float (&dy)[VEC]) const {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) x[j] = h(j, x[j]);
+    if (!SILU) return;
+    if (T::kWide) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        dy[j] = mul_alone(dy[j], silu_slope<true>(fmaf(x[j], gamma[j], beta[j])));
+      return;
+    }
+    constexpr float kLn2 = 0.693147182464599609375f;
+    float p[VEC], t[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) p[j] = fmaf(x[j], gamma[j], beta[j]);
+    step_edge();
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) t[j] = __builtin_amdgcn_exp2f(p[j]);
+    step_edge();
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) t[j] += 1.0f;
+    step_edge();
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) t[j] = __builtin_amdgcn_rcpf(t[j]);
+    step_edge();
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) p[j] = fmaf(p[j], fmaf(t[j], kLn2, -kLn2), 1.0f);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) dy[j] = mul_alone(dy[j], t[j] * p[j]);
+    step_edge();
+  }
+};
+
+// R <= 4 rows: few values, where the terms of dx may cancel: gn_dx, and da
+// formed again. More rows: da stays in registers in the place of dy, and dx is
+// two products per value. GV groups at most share a vector's channels: VEC, or
+// a quarter of that where every four channels are of one group.
+template <class T, bool SILU, int R, int GV>
+__global__ __launch_bounds__(kGnResThreadsBwd, 2) void gn_resident_bwd_kernel(GnTrainArgs a,
+                                                                              GnResPlan r) {
   typedef typename T::store E;
-  constexpr int VEC = 16 / sizeof(E);
-  constexpr int NT = kGnResThreadsBwd;
+  constexpr int VEC = 16 / sizeof(E), NT = kGnResThreadsBwd;
+  constexpr bool FEW = R <= 4;
   __shared__ ChannelSums<NT, 2, VEC> sums;
   __shared__ unsigned long long xw[kGnResWords];
-  __shared__ float g1[NT], g2[NT];
+  __shared__ float g1[NT], g2[NT], lgamma[NT];
   __shared__ int late;
   const Where h = where(r);
   const int c0 = h.range * r.Cb + h.cv * VEC, gl0 = h.cv * VEC;
@@ -351,125 +571,156 @@ __global__ __launch_bounds__(kGnResThreadsBwd, 2) void gn_resident_bwd_kernel(Gn
   long long first;
   const int n = rows_of(a, r, h, h.w, &first);
   Held<T> vx[R], vd[R];
-  float mean[VEC], rstd[VEC], gamma[VEC], beta[VEC];
+  float vda[FEW ? 1 : R][VEC];
+  BwdValues<T, SILU, VEC, GV> bv;
   if (threadIdx.x == 0) late = 0;
-  load_rows<T, R>(a.x, a.x_pitch, at, c0, first, r.ppi, n, vx);
-  load_rows<T, R>(a.dy, a.dy_pitch, at, c0, first, r.ppi, n, vd);
+  // ahead of the rows, as in the forward pass
+  if (threadIdx.x < r.Cb) lgamma[threadIdx.x] = a.gamma[h.range * r.Cb + threadIdx.x];
+  {
+    GroupOf go(h.active ? gl0 : 0, a.cpg);
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    const int g = h.active ? (gl0 + j) / a.cpg : 0, c = h.active ? c0 + j : 0;
-    mean[j] = st[g * 2];
-    rstd[j] = st[g * 2 + 1];
-    gamma[j] = a.gamma[c];
-    beta[j] = a.beta[c];
+    for (int j = 0; j < VEC; ++j) {
+      const int g = go.next(a.cpg), c = h.active ? c0 + j : 0;
+      bv.init(j, st[g * 2], st[g * 2 + 1], a.gamma[c], a.beta[c]);
+    }
   }
-  const auto value = [&](int j, float x, float dy, float& hh, float& da) {
-    hh = mul_alone(x - mean[j], rstd[j]);
-    da = SILU ? mul_alone(dy, silu_slope<T::kWide>(fmaf(hh, gamma[j], beta[j]))) : dy;
-  };
-  // (sum of gamma da, of gamma da h) of a piece's groups, as words
-  const auto piece = [&](unsigned long long* out, auto rows) {
-    float s[2][VEC];
+  {
+    const E* px = (const E*)a.x + (at + first) * a.x_pitch + c0;
+    const E* pd = (const E*)a.dy + (at + first) * a.dy_pitch + c0;
+    const long long sx = r.ppi * a.x_pitch, sd = r.ppi * a.dy_pitch;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) s[0][j] = s[1][j] = 0.0f;
-    rows([&](const Held<T>& rx, const Held<T>& rd) {
-      float f[VEC], d[VEC];
-      rx.get(f);
-      rd.get(d);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        float hh, da;
-        value(j, f[j], d[j], hh, da);
-        s[0][j] = fmaf(da, hh, s[0][j]);
-        s[1][j] += da;
+    for (int i = 0; i < R; ++i) {
+      if (i < n) {
+        vx[i].v = *(const u32x4_t*)px;
+        vd[i].v = *(const u32x4_t*)pd;
       }
-    });
+      px += sx;
+      pd += sd;
+    }
+  }
+  // (sum of gamma da, of gamma da h) of a piece's groups, as words
+  const auto piece = [&](unsigned long long* out, float (&s)[2][VEC]) {
     sums.join(r, h.active, s);
-    const float* gm = a.gamma + h.range * r.Cb;
-    each_group<NT>(r.Gb, a.cpg, [&](int c) { return mul_alone(gm[c], sums.tot[1][c]); },
-               [&](int g, float t) { g1[g] = t; });
-    each_group<NT>(r.Gb, a.cpg, [&](int c) { return mul_alone(gm[c], sums.tot[0][c]); },
-               [&](int g, float t) { g2[g] = t; });
+    each_group<NT>(r.Gb, a.cpg, [&](int c) { return mul_alone(lgamma[c], sums.tot[1][c]); },
+                   [&](int g, float t) { g1[g] = t; });
+    each_group<NT>(r.Gb, a.cpg, [&](int c) { return mul_alone(lgamma[c], sums.tot[0][c]); },
+                   [&](int g, float t) { g2[g] = t; });
     __syncthreads();
     for (int g = threadIdx.x; g < r.Gb; g += NT) out[g] = word_of(g1[g], g2[g]);
   };
-  piece(xw + h.w * r.Gb, [&](auto f) {
+  const auto add = [&](float (&s)[2][VEC], int j, float hh, float da) {
+    s[0][j] = fmaf(da, hh, s[0][j]);
+    s[1][j] += da;
+  };
+  float s[2][VEC];
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (i < n) f(vx[i], vd[i]);
-  });
-  if (r.channel_sums) {
-    float* row = r.channel_sums + ((long long)h.u * r.W + h.w) * 2 * a.C + h.range * r.Cb;
-    if (threadIdx.x < r.Cb) {
-      row[threadIdx.x] = sums.tot[0][threadIdx.x];
-      row[a.C + threadIdx.x] = sums.tot[1][threadIdx.x];
+  for (int j = 0; j < VEC; ++j) s[0][j] = s[1][j] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (i < n) {
+      float f[VEC], d[VEC];
+      vx[i].get(f);
+      vd[i].get(d);
+      bv.run(f, d);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        add(s, j, f[j], d[j]);
+        if (!FEW) vda[FEW ? 0 : i][j] = d[j];
+      }
     }
   }
+  piece(xw + h.w * r.Gb, s);
+  if (r.channel_sums && threadIdx.x < r.Cb) {
+    float* row = r.channel_sums + ((long long)h.u * r.W + h.w) * 2 * a.C + h.range * r.Cb;
+    row[threadIdx.x] = sums.tot[0][threadIdx.x];
+    row[a.C + threadIdx.x] = sums.tot[1][threadIdx.x];
+  }
   if (!a.out) return;
-  __syncthreads();
   if (r.W > 1) {
-    unsigned long long* words =
-        r.words + ((long long)h.u * r.NR + h.range) * r.W * r.Gb;
-    for (int g = threadIdx.x; g < r.Gb; g += NT)
-      __hip_atomic_store(words + h.w * r.Gb + g, xw[h.w * r.Gb + g], __ATOMIC_RELAXED,
-                         __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    if (!gather<NT>(words, r.W * r.Gb, r.spin, xw, &late)) {
+    if (!exchange<NT>(r, h, xw, &late)) {
       for (int w = 0; w < r.W; ++w) {
         long long fw;
         const int nw = rows_of(a, r, h, w, &fw);
         const E* px = (const E*)a.x + (at + fw) * a.x_pitch + c0;
         const E* pd = (const E*)a.dy + (at + fw) * a.dy_pitch + c0;
-        piece(xw + w * r.Gb, [&](auto f) {
+        const long long sx = r.ppi * a.x_pitch, sd = r.ppi * a.dy_pitch;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) s[0][j] = s[1][j] = 0.0f;
 #pragma unroll 1
-          for (int i = 0; i < nw; ++i) {
-            Held<T> x1, d1;
-            x1.v = *(const u32x4_t*)(px + i * (r.ppi * a.x_pitch));
-            d1.v = *(const u32x4_t*)(pd + i * (r.ppi * a.dy_pitch));
-            f(x1, d1);
-          }
-        });
+        for (int i = 0; i < nw; ++i) {
+          Held<T> x1, d1;
+          x1.v = *(const u32x4_t*)(px + i * sx);
+          d1.v = *(const u32x4_t*)(pd + i * sd);
+          float f[VEC], d[VEC];
+          x1.get(f);
+          d1.get(d);
+          bv.run(f, d);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) add(s, j, f[j], d[j]);
+        }
+        piece(xw + w * r.Gb, s);
       }
-      __syncthreads();
-    }
-  }
-  for (int g = threadIdx.x >> 6; g < r.Gb; g += NT / 64) {
-    const int lane = threadIdx.x & 63;
-    const double N = (double)a.P * a.cpg;
-    double s1 = 0.0, s2 = 0.0;
-    for (int w = lane; w < r.W; w += 64) {
-      s1 += (double)word_lo(xw[w * r.Gb + g]);
-      s2 += (double)word_hi(xw[w * r.Gb + g]);
-    }
-    s1 = wave_sum(s1);
-    s2 = wave_sum(s2);
-    if (lane == 0) {
-      g1[g] = (float)(s1 / N);
-      g2[g] = (float)(s2 / N);
     }
   }
   __syncthreads();
+  const double inv_n = 1.0 / ((double)a.P * a.cpg);
+  const double N = (double)a.P * a.cpg;
+  over_pieces<NT>(
+      r,
+      [&](int g, int lane, int lg) {
+        double s1 = 0.0, s2 = 0.0;
+        for (int w = lane; w < r.W; w += lg) {
+          s1 += (double)word_lo(xw[w * r.Gb + g]);
+          s2 += (double)word_hi(xw[w * r.Gb + g]);
+        }
+        return double2{lanes_sum(s1, lg), lanes_sum(s2, lg)};
+      },
+      [&](int g, int lane, double2 t) {
+        if (lane == 0) {
+          g1[g] = (float)(FEW ? t.x / N : t.x * inv_n);
+          g2[g] = (float)(FEW ? t.y / N : t.y * inv_n);
+        }
+      });
+  __syncthreads();
   if (!h.active) return;
-  float c1[VEC], c2[VEC];
+  float c1[VEC], c2[VEC], gam[VEC];
+  GroupOf go(gl0, a.cpg);
 #pragma unroll
   for (int j = 0; j < VEC; ++j) {
-    c1[j] = g1[(gl0 + j) / a.cpg];
-    c2[j] = g2[(gl0 + j) / a.cpg];
+    const int g = go.next(a.cpg);
+    c1[j] = g1[g];
+    c2[j] = g2[g];
+    gam[j] = lgamma[gl0 + j];
+    if (!FEW) {
+      // dx = (rstd gamma) da - (rstd c2) h - rstd c1; 16-bit types: h spelt out in x
+      const float rs = bv.rstd[bv.at(j)];
+      gam[j] = rs * gam[j];
+      c2[j] = -rs * c2[j];
+      c1[j] = -rs * c1[j];
+      if (!T::kWide) {
+        c1[j] = fmaf(bv.mean[bv.at(j)], c2[j], c1[j]);
+        c2[j] = rs * c2[j];
+      }
+    }
   }
   E* dx = (E*)a.out + (at + first) * a.out_pitch + c0;
   const long long step = r.ppi * a.out_pitch;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    __builtin_amdgcn_sched_barrier(0);
     if (i < n) {
       float f[VEC], d[VEC];
       vx[i].get(f);
-      vd[i].get(d);
+      if (FEW) {
+        vd[i].get(d);
+        bv.run(f, d);
+      }
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        float hh, da;
-        value(j, f[j], d[j], hh, da);
-        f[j] = gn_dx(rstd[j], gamma[j], da, c1[j], hh, c2[j]);
+        if (FEW)
+          f[j] = gn_dx(bv.rstd[bv.at(j)], gam[j], d[j], c1[j], f[j], c2[j]);
+        else
+          f[j] = fmaf(vda[FEW ? 0 : i][j], gam[j],
+                      fmaf(T::kWide ? bv.h(j, f[j]) : f[j], c2[j], c1[j]));
       }
       Held<T> o;
       o.put(f);
@@ -492,19 +743,25 @@ int run_fwd(const GnTrainArgs& a, const GnResPlan& r, hipStream_t s) {
   if (r.passes <= 4)
     hipLaunchKernelGGL((gn_resident_fwd_kernel<T, SILU, 4>), grid, block, 0, s, a, r);
   else
-    hipLaunchKernelGGL((gn_resident_fwd_kernel<T, SILU, kGnResRows>), grid, block, 0, s, a, r);
+    hipLaunchKernelGGL((gn_resident_fwd_kernel<T, SILU, kGnResRowsFwd>), grid, block, 0, s, a, r);
   return (int)hipGetLastError();
+}
+
+template <class T, bool SILU, int R>
+void start_bwd(const GnTrainArgs& a, const GnResPlan& r, hipStream_t s) {
+  constexpr int VEC = 16 / sizeof(typename T::store);
+  const dim3 grid(a.units * r.NR * r.W), block(kGnResThreadsBwd);
+  if (r.fold >= 4)
+    hipLaunchKernelGGL((gn_resident_bwd_kernel<T, SILU, R, VEC / 4>), grid, block, 0, s, a, r);
+  else
+    hipLaunchKernelGGL((gn_resident_bwd_kernel<T, SILU, R, VEC>), grid, block, 0, s, a, r);
 }
 
 template <class T, bool SILU>
 int run_bwd(const GnTrainArgs& a, const GnResPlan& r, hipStream_t s) {
   if (r.W > 1 && a.out) clear_words(a, r, s);
-  const dim3 grid(a.units * r.NR * r.W);
-  const dim3 block(kGnResThreadsBwd);
-  if (r.passes <= 4)
-    hipLaunchKernelGGL((gn_resident_bwd_kernel<T, SILU, 4>), grid, block, 0, s, a, r);
-  else
-    hipLaunchKernelGGL((gn_resident_bwd_kernel<T, SILU, kGnResRows>), grid, block, 0, s, a, r);
+  if (r.passes <= 4) start_bwd<T, SILU, 4>(a, r, s);
+  else start_bwd<T, SILU, kGnResRowsBwd>(a, r, s);
   if (r.channel_sums)
     hipLaunchKernelGGL(column_sums_kernel, dim3((2 * a.C + kSumCols - 1) / kSumCols),
                        dim3(kSumThreads), 0, s, r.channel_sums, a.units * r.W, a.C, a.dgamma,

@@ -44,12 +44,15 @@ int launch_gn_train_bwd(const GnTrainArgs& args, void* stream);
 // (Cb channels in Vb 16-byte vectors), NR of them make C; the unit's pixels
 // are cut into W pieces of piece_px = ppi * passes.
 constexpr int kGnResThreadsFwd = 512, kGnResThreadsBwd = 256;
-constexpr int kGnResRows = 16;                         // rows a thread can hold
-constexpr int kGnResWords = 2048;                      // words of one exchange
+constexpr int kGnResRowsFwd = 16, kGnResRowsBwd = 12;  // rows a thread can hold
+constexpr int kGnResWords = 4096;                      // words of one exchange
 struct GnResPlan {
   int Cb, Vb, NR, Gb;
   int ppi, passes, piece_px, W;
-  int parts;                 // lanes of rows that join a channel's sums
+  int lanes;                 // 1: a row is a power of two of lanes (at most a wave)
+  int fold;                  // channels of a vector that always share a group (a power of two)
+  int entry_lanes;           // lanes that join one group's rows of a piece (a power of two)
+  int join_lanes;            // lanes that join one group's pieces (a power of two)
   int spin;                  // polls of one word before a work-group helps itself
   unsigned long long* words; // [units][NR][W][Gb] (W > 1)
   float* channel_sums;       // backward: [units][W][2][C], or null

@@ -33,7 +33,7 @@ struct GnTrainPlan {
   size_t off_sums;
 };
 
-constexpr int kGnMaxPieces = 128;        // of one exchange; 512 work-groups are resident
+constexpr int kGnMaxPieces = 256;        // of one exchange; 512 work-groups are resident
 constexpr int kGnFill = 512;             // work-groups that fill the chip
 constexpr int kGnSpin = 20000;           // polls (about a microsecond each) before helping oneself
 
@@ -43,7 +43,8 @@ int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 // unit's pieces are too many to be on the chip together.
 bool plan_resident(const GnTrainArgs& a, bool bwd, GnResPlan* r) {
   const int size = elt_size(a.dtype), vec = 16 / size;
-  const int rows = kGnResRows, threads = bwd ? kGnResThreadsBwd : kGnResThreadsFwd;
+  const int rows = bwd ? kGnResRowsBwd : kGnResRowsFwd;
+  const int threads = bwd ? kGnResThreadsBwd : kGnResThreadsFwd;
   if (a.C % vec) return false;
   const int quantum = a.cpg / gcd(a.cpg, vec) * vec;    // whole groups in whole vectors
   const auto lay = [&](int Cb) {
@@ -52,7 +53,16 @@ bool plan_resident(const GnTrainArgs& a, bool bwd, GnResPlan* r) {
     r->NR = a.C / Cb;
     r->Gb = Cb / a.cpg;
     r->ppi = threads / r->Vb;
-    r->parts = std::min(threads / Cb, r->ppi);
+    r->lanes = r->Vb <= 64 && (r->Vb & (r->Vb - 1)) == 0;
+    r->fold = 1;
+    while (r->fold < vec && a.cpg % (2 * r->fold) == 0) r->fold *= 2;
+    const int entries = (r->lanes ? threads / 64 : r->ppi) * (a.cpg / r->fold);
+    r->entry_lanes = 1;
+    while (r->entry_lanes < 32 && 2 * r->entry_lanes <= entries &&
+           2 * r->entry_lanes * r->Gb <= threads)
+      r->entry_lanes *= 2;
+    r->join_lanes = 64;
+    while (r->join_lanes > 1 && r->join_lanes * r->Gb > threads) r->join_lanes /= 2;
   };
   const int limit = std::min(a.C, threads);
   // one work-group per range: the narrowest range of at least 64 bytes a pixel
