@@ -103,11 +103,6 @@ struct GroupOf {
   }
 };
 
-__device__ __forceinline__ double lanes_sum(double v, int lanes) {
-  for (int m = lanes >> 1; m > 0; m >>= 1) v += __shfl_xor(v, m);
-  return v;
-}
-
 // ---- joining a work-group's rows
 //
 // Where a row's vectors are a power of two of lanes, rows of one wave are
@@ -115,22 +110,25 @@ __device__ __forceinline__ double lanes_sum(double v, int lanes) {
 // LDS; else every lane's goes. Either way in a fixed order.
 
 // Channel sums of N quantities: s[k][j] of every thread -> tot[k][channel].
-template <int NT, int N, int VEC>
+// COMPACT (the lanes' form, at most kGnCompact values of a row): small arrays,
+// and the space is left to rows.
+template <int NT, int N, int VEC, bool COMPACT>
 struct ChannelSums {
-  float red[N][NT * VEC];
-  float tot[N][NT];
+  float red[N][COMPACT ? NT / 64 * kGnCompact : NT * VEC];
+  float tot[N][COMPACT ? kGnCompact : NT];
   __device__ __forceinline__ void join(const GnResPlan& r, bool active, float (&s)[N][VEC]) {
     const int t = threadIdx.x;
-    if (r.lanes) {
+    const bool lanes = COMPACT || r.lanes;
+    if (lanes) {
       for (int m = r.Vb; m < 64; m <<= 1)
 #pragma unroll
         for (int k = 0; k < N; ++k)
 #pragma unroll
           for (int j = 0; j < VEC; ++j) s[k][j] += __shfl_xor(s[k][j], m);
     }
-    const int rows = r.lanes ? NT / 64 : r.ppi;
-    const int at = r.lanes ? (t >> 6) * r.Cb + (t & 63) * VEC : t * VEC;
-    if (r.lanes ? (t & 63) < r.Vb : active) {
+    const int rows = lanes ? NT / 64 : r.ppi;
+    const int at = lanes ? (t >> 6) * r.Cb + (t & 63) * VEC : t * VEC;
+    if (lanes ? (t & 63) < r.Vb : active) {
 #pragma unroll
       for (int k = 0; k < N; ++k)
 #pragma unroll
@@ -164,9 +162,10 @@ struct Moments {
 
 // (mean, squares about it) of the groups of a piece to use(g, mean, m2), from
 // one Moments per slot (`fold` channels of one group) and wave (or lane row).
-template <int NT, int VEC>
+template <int NT, int VEC, bool COMPACT>
 struct GroupMoments {
-  float mean[NT * VEC], m2[NT * VEC];
+  static constexpr int kSize = COMPACT ? NT / 64 * kGnCompact : NT * VEC;
+  float mean[kSize], m2[kSize];
   float n[NT];
   template <class Use>
   __device__ __forceinline__ void join(const GnResPlan& r, int cpg, bool active, int rows,
@@ -185,7 +184,8 @@ struct GroupMoments {
         }
         cnt *= 2.0f;
       }
-    if (r.lanes) {
+    const bool lanes = COMPACT || r.lanes;
+    if (lanes) {
       for (int m = r.Vb; m < 64; m <<= 1) {
         const float on = __shfl_xor(cnt, m);
         const bool low = (t & m) == 0;          // both lanes join in the same order
@@ -203,11 +203,11 @@ struct GroupMoments {
         cnt += on;
       }
     }
-    const int nrow = r.lanes ? NT / 64 : r.ppi;
+    const int nrow = lanes ? NT / 64 : r.ppi;
     const int slots = VEC / r.fold;             // of a thread's vector
     const int width = r.Vb * slots;
-    const int lane = r.lanes ? t & 63 : t % r.Vb, row = r.lanes ? t >> 6 : t / r.Vb;
-    if (r.lanes ? lane < r.Vb : active) {
+    const int lane = lanes ? t & 63 : t % r.Vb, row = lanes ? t >> 6 : t / r.Vb;
+    if (lanes ? lane < r.Vb : active) {
       n[row * r.Vb + lane] = cnt;
       int at = row * width + lane * slots;
 #pragma unroll
@@ -273,71 +273,108 @@ __device__ __forceinline__ void each_group(int Gb, int cpg, Value value, Use use
 
 // ---- the exchange
 
-// Publishes this piece's words, which LDS holds, and adds those of the other
-// pieces of the (unit, range); false where one stayed empty.
+// Sums over the pieces of a (unit, range), in fp64. Thread t takes group t %
+// Gb and every LG-th piece from t / Gb on (LG = NT / Gb), so a work-group's
+// reads of the words are contiguous; the threads' sums are joined in order.
 template <int NT>
-__device__ __forceinline__ bool exchange(const GnResPlan& r, const Where& h,
-                                         unsigned long long* xw, int* late) {
-  unsigned long long* words = r.words + ((long long)h.u * r.NR + h.range) * r.W * r.Gb;
-  const int own = h.w * r.Gb, n = r.W * r.Gb;
-  for (int i = own + threadIdx.x; i < own + r.Gb; i += NT)
-    __hip_atomic_store(words + i, xw[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  // four words in flight per thread: a poll is a trip to memory
-  for (int i0 = threadIdx.x; i0 < n; i0 += 4 * NT) {
-    unsigned long long v[4];
-    bool open[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int i = i0 + q * NT;
-      open[q] = i < n && !(i >= own && i < own + r.Gb);
-      v[q] = kEmpty;
-    }
-    for (int k = 0; k < r.spin; ++k) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (open[q])
-          v[q] = __hip_atomic_load(words + i0 + q * NT, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      bool wait = false;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (open[q] && v[q] != kEmpty) {
-          xw[i0 + q * NT] = v[q];
-          open[q] = false;
-        }
-        wait |= open[q];
-      }
-      if (!wait) break;
-    }
-    if (open[0] | open[1] | open[2] | open[3]) *late = 1;
-  }
-  __syncthreads();
-  return *late == 0;
-}
+struct PieceSums {
+  double a[NT], b[NT];
+  unsigned long long own[NT];    // one piece's words
+  int late;
 
-// f(g, lane) -> two sums over the pieces of group g, in fp64: as many lanes
-// per group (a power of two, at most a wave) as the work-group has.
-template <int NT, class F, class Use>
-__device__ __forceinline__ void over_pieces(const GnResPlan& r, F f, Use use) {
-  const int lg = r.join_lanes;
-  const int lane = threadIdx.x & (lg - 1);
-  for (int g = threadIdx.x / lg; g < r.Gb; g += NT / lg) use(g, lane, f(g, lane, lg));
-}
+  // Publishes this piece's words (in own, visible to all threads) and calls
+  // add(w, word) for the thread's group and pieces in ascending order; false
+  // where a piece's word stayed empty, and then nothing is to be believed.
+  template <class Add>
+  __device__ __forceinline__ bool collect(const GnResPlan& r, const Where& h, Add add) {
+    const int t = threadIdx.x;
+    unsigned long long* words = r.words + ((long long)h.u * r.NR + h.range) * r.W * r.Gb;
+    if (t == 0) late = 0;
+    for (int g = t; g < r.Gb; g += NT)
+      __hip_atomic_store(words + h.w * r.Gb + g, own[g], __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    const int LG = NT / r.Gb, slot = t / r.Gb, g = t - slot * r.Gb;
+    // two words in flight per thread: a poll is a trip to memory, behind the
+    // rows that the other work-group on this CU has asked for
+    for (int w0 = slot < LG ? slot : r.W; w0 < r.W; w0 += 2 * LG) {
+      const int w1 = w0 + LG;
+      bool open0 = w0 != h.w, open1 = w1 < r.W && w1 != h.w;
+      unsigned long long v0 = own[g], v1 = v0;
+      for (int k = 0; k < r.spin && (open0 | open1); ++k) {
+        if (open0)
+          v0 = __hip_atomic_load(words + w0 * r.Gb + g, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (open1)
+          v1 = __hip_atomic_load(words + w1 * r.Gb + g, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        open0 = open0 && v0 == kEmpty;
+        open1 = open1 && v1 == kEmpty;
+      }
+      if (open0 | open1) late = 1;
+      add(w0, v0);
+      if (w1 < r.W) add(w1, v1);
+    }
+    __syncthreads();
+    return late == 0;
+  }
+
+  // add() of one piece whose words are in own, for the threads that take it.
+  template <class Add>
+  __device__ __forceinline__ void one(const GnResPlan& r, int w, Add add) {
+    const int LG = NT / r.Gb, slot = threadIdx.x / r.Gb;
+    if (slot < LG && w % LG == slot) add(w, own[threadIdx.x - slot * r.Gb]);
+    __syncthreads();
+  }
+
+  // The threads' sums joined per group, to use(g, sum, sum).
+  template <class Use>
+  __device__ __forceinline__ void join(const GnResPlan& r, double s1, double s2, Use use) {
+    const int t = threadIdx.x;
+    a[t] = s1;
+    b[t] = s2;
+    __syncthreads();
+    const int LG = min(NT / r.Gb, r.W);
+    if (LG <= 32) {
+      for (int g = t; g < r.Gb; g += NT) {
+        double x = a[g], y = b[g];
+        for (int i = 1; i < LG; ++i) {
+          x += a[i * r.Gb + g];
+          y += b[i * r.Gb + g];
+        }
+        use(g, x, y);
+      }
+    } else {
+      for (int g = t >> 6; g < r.Gb; g += NT / 64) {
+        double x = 0.0, y = 0.0;
+        for (int i = t & 63; i < LG; i += 64) {
+          x += a[i * r.Gb + g];
+          y += b[i * r.Gb + g];
+        }
+        x = wave_sum(x);
+        y = wave_sum(y);
+        if ((t & 63) == 0) use(g, x, y);
+      }
+    }
+    __syncthreads();
+  }
+};
+
 // Steps of a vector's values are kept apart from each other: the compiler
 // would chain one value's exponential and reciprocal after another's to save
 // registers, and wait for each (two waves per SIMD hide nothing: 7.5 us of a
 // piece's 23).
 __device__ __forceinline__ void step_edge() { __builtin_amdgcn_sched_barrier(0); }
 
-template <class T, bool SILU, int R>
+// R rows of which LROWS are kept in LDS.
+template <class T, bool SILU, int R, int LROWS, bool COMPACT>
 __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(GnTrainArgs a,
                                                                               GnResPlan r) {
   typedef typename T::store E;
   constexpr int VEC = 16 / sizeof(E), NT = kGnResThreadsFwd;
-  __shared__ GroupMoments<NT, VEC> sums;
-  __shared__ unsigned long long xw[kGnResWords];
+  __shared__ GroupMoments<NT, VEC, COMPACT> sums;
+  __shared__ u32x4_t lds_x[LROWS ? LROWS : 1][LROWS ? NT : 1];
+  __shared__ PieceSums<NT> pieces;
   __shared__ float gmean[NT], grstd[NT];
   __shared__ float lgamma[NT], lbeta[NT];
-  __shared__ int late;
   const Where h = where(r);
   // ahead of the rows: a load that is issued later returns after all of them,
   // and after those of the other work-group on this CU
@@ -350,12 +387,11 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
   long long first;
   const int n = rows_of(a, r, h, h.w, &first);
   Held<T> v[R];
-  if (threadIdx.x == 0) late = 0;
 
   // Per channel, sums about the thread's first value (no cancellation where
   // the mean is far above the spread) -> the piece's group moments as words.
   // rows(f) visits the thread's rows of the piece.
-  const auto piece = [&](unsigned long long* out, int n, const Held<T>& v0, auto rows) {
+  const auto piece = [&](int n, const Held<T>& v0, auto rows) {
     float sh[VEC], s1[VEC], s2[VEC];
     v0.get(sh);
 #pragma unroll
@@ -379,7 +415,7 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
       m[j].m2 = fmaf(-d, s1[j], s2[j]);
       m[j].m2 = m[j].m2 < 0.0f ? 0.0f : m[j].m2;      // and not fmaxf: a NaN stays
     }
-    sums.join(r, a.cpg, h.active, n, m, [&](int g, float mu, float q) { out[g] = word_of(mu, q); });
+    sums.join(r, a.cpg, h.active, n, m, [&](int g, float mu, float q) { pieces.own[g] = word_of(mu, q); });
   };
 
   {
@@ -392,13 +428,37 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
       p += step;
     }
   }
-  piece(xw + h.w * r.Gb, n, v[0], [&](auto f) {
+  piece(n, v[0], [&](auto f) {
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int i = 0; i < R; ++i) {
       if (i < n) f(v[i]);
+      if (i < LROWS) lds_x[i][threadIdx.x] = v[i].v;
+    }
   });
-  if (r.W > 1) {
-    if (!exchange<NT>(r, h, xw, &late)) {
+  // pieces joined by the sums of n mean and of squares + n mean^2
+  const double full = (double)r.piece_px * a.cpg;
+  const double last = (double)(a.P - (long long)(r.W - 1) * r.piece_px) * a.cpg;
+  const double inv_n = 1.0 / ((double)a.P * a.cpg);
+  const auto group = [&](int g, double s1, double s2) {
+    const double mean = s1 * inv_n, var = s2 * inv_n - mean * mean;
+    gmean[g] = (float)mean;
+    grstd[g] = (float)(1.0 / sqrt((var < 0.0 ? 0.0 : var) + (double)a.eps));  // a NaN stays
+  };
+  if (r.W == 1) {
+    for (int g = threadIdx.x; g < r.Gb; g += NT) {
+      const double mean = word_lo(pieces.own[g]);
+      group(g, mean * last, (double)word_hi(pieces.own[g]) + mean * mean * last);
+    }
+    __syncthreads();
+  } else {
+    double s1 = 0.0, s2 = 0.0;
+    const auto add = [&](int w, unsigned long long x) {
+      const double mean = word_lo(x), nm = (w == r.W - 1 ? last : full) * mean;
+      s1 += nm;
+      s2 += (double)word_hi(x) + nm * mean;
+    };
+    if (!pieces.collect(r, h, add)) {
+      s1 = s2 = 0.0;
       for (int w = 0; w < r.W; ++w) {
         long long fw;
         const int nw = rows_of(a, r, h, w, &fw);
@@ -407,7 +467,7 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
         Held<T> v0;
         v0.v = u32x4_t{0, 0, 0, 0};
         if (nw > 0) v0.v = *(const u32x4_t*)p;
-        piece(xw + w * r.Gb, nw, v0, [&](auto f) {
+        piece(nw, v0, [&](auto f) {
 #pragma unroll 1
           for (int i = 0; i < nw; ++i) {
             Held<T> row;
@@ -415,35 +475,11 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
             f(row);
           }
         });
+        pieces.one(r, w, add);
       }
     }
+    pieces.join(r, s1, s2, group);
   }
-  const double full = (double)r.piece_px * a.cpg;
-  const double last = (double)(a.P - (long long)(r.W - 1) * r.piece_px) * a.cpg;
-  const double inv_n = 1.0 / ((double)a.P * a.cpg);
-  over_pieces<NT>(
-      r,
-      [&](int g, int lane, int lg) {
-        // about the first piece's mean, so both sums are formed at once
-        const double k = (double)word_lo(xw[g]);
-        double s1 = 0.0, s2 = 0.0;
-        for (int w = lane; w < r.W; w += lg) {
-          const unsigned long long x = xw[w * r.Gb + g];
-          const double d = (double)word_lo(x) - k, nd = (w == r.W - 1 ? last : full) * d;
-          s1 += nd;
-          s2 += (double)word_hi(x) + nd * d;
-        }
-        s1 = lanes_sum(s1, lg) * inv_n;
-        const double var = lanes_sum(s2, lg) * inv_n - s1 * s1;
-        return double2{k + s1, var < 0.0 ? 0.0 : var};        // and not fmax: a NaN stays
-      },
-      [&](int g, int lane, double2 mv) {
-        if (lane == 0) {
-          gmean[g] = (float)mv.x;
-          grstd[g] = (float)(1.0 / sqrt(mv.y + (double)a.eps));
-        }
-      });
-  __syncthreads();
   if (h.w == 0) {
     float* st = a.stats + ((long long)h.u * a.G + h.range * r.Gb) * 2;
     for (int g = threadIdx.x; g < r.Gb; g += NT) {
@@ -471,6 +507,7 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
   for (int i = 0; i < R; ++i) {
     if (i < n) {
       float f[VEC];
+      if (i < LROWS) v[i].v = lds_x[i][threadIdx.x];
       v[i].get(f);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
@@ -551,19 +588,19 @@ struct BwdValues {
 };
 
 // R <= 4 rows: few values, where the terms of dx may cancel: gn_dx, and da
-// formed again. More rows: da stays in registers in the place of dy, and dx is
-// two products per value. GV groups at most share a vector's channels: VEC, or
+// formed again. More rows: da is kept in the place of dy, of LROWS rows in LDS,
+// and dx is two products per value. GV groups at most share a vector's channels: VEC, or
 // a quarter of that where every four channels are of one group.
-template <class T, bool SILU, int R, int GV>
+template <class T, bool SILU, int R, int LROWS, int GV, bool COMPACT>
 __global__ __launch_bounds__(kGnResThreadsBwd, 2) void gn_resident_bwd_kernel(GnTrainArgs a,
                                                                               GnResPlan r) {
   typedef typename T::store E;
   constexpr int VEC = 16 / sizeof(E), NT = kGnResThreadsBwd;
   constexpr bool FEW = R <= 4;
-  __shared__ ChannelSums<NT, 2, VEC> sums;
-  __shared__ unsigned long long xw[kGnResWords];
+  __shared__ ChannelSums<NT, 2, VEC, COMPACT> sums;
+  __shared__ PieceSums<NT> pieces;
+  __shared__ f32x4_t lds_da[LROWS ? LROWS : 1][VEC / 4][LROWS ? NT : 1];
   __shared__ float g1[NT], g2[NT], lgamma[NT];
-  __shared__ int late;
   const Where h = where(r);
   const int c0 = h.range * r.Cb + h.cv * VEC, gl0 = h.cv * VEC;
   const long long at = (long long)h.u * a.P;
@@ -571,9 +608,8 @@ __global__ __launch_bounds__(kGnResThreadsBwd, 2) void gn_resident_bwd_kernel(Gn
   long long first;
   const int n = rows_of(a, r, h, h.w, &first);
   Held<T> vx[R], vd[R];
-  float vda[FEW ? 1 : R][VEC];
+  float vda[FEW ? 1 : R - LROWS][VEC];
   BwdValues<T, SILU, VEC, GV> bv;
-  if (threadIdx.x == 0) late = 0;
   // ahead of the rows, as in the forward pass
   if (threadIdx.x < r.Cb) lgamma[threadIdx.x] = a.gamma[h.range * r.Cb + threadIdx.x];
   {
@@ -599,14 +635,15 @@ __global__ __launch_bounds__(kGnResThreadsBwd, 2) void gn_resident_bwd_kernel(Gn
     }
   }
   // (sum of gamma da, of gamma da h) of a piece's groups, as words
-  const auto piece = [&](unsigned long long* out, float (&s)[2][VEC]) {
+  const auto piece = [&](float (&s)[2][VEC]) {
     sums.join(r, h.active, s);
     each_group<NT>(r.Gb, a.cpg, [&](int c) { return mul_alone(lgamma[c], sums.tot[1][c]); },
                    [&](int g, float t) { g1[g] = t; });
     each_group<NT>(r.Gb, a.cpg, [&](int c) { return mul_alone(lgamma[c], sums.tot[0][c]); },
                    [&](int g, float t) { g2[g] = t; });
     __syncthreads();
-    for (int g = threadIdx.x; g < r.Gb; g += NT) out[g] = word_of(g1[g], g2[g]);
+    for (int g = threadIdx.x; g < r.Gb; g += NT) pieces.own[g] = word_of(g1[g], g2[g]);
+    __syncthreads();
   };
   const auto add = [&](float (&s)[2][VEC], int j, float hh, float da) {
     s[0][j] = fmaf(da, hh, s[0][j]);
@@ -625,19 +662,39 @@ __global__ __launch_bounds__(kGnResThreadsBwd, 2) void gn_resident_bwd_kernel(Gn
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         add(s, j, f[j], d[j]);
-        if (!FEW) vda[FEW ? 0 : i][j] = d[j];
+        if (!FEW && i >= LROWS) vda[FEW ? 0 : i - LROWS][j] = d[j];
+      }
+      if (i < LROWS) {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 4)
+          lds_da[i][j / 4][threadIdx.x] = f32x4_t{d[j], d[j + 1], d[j + 2], d[j + 3]};
       }
     }
   }
-  piece(xw + h.w * r.Gb, s);
+  piece(s);
   if (r.channel_sums && threadIdx.x < r.Cb) {
     float* row = r.channel_sums + ((long long)h.u * r.W + h.w) * 2 * a.C + h.range * r.Cb;
     row[threadIdx.x] = sums.tot[0][threadIdx.x];
     row[a.C + threadIdx.x] = sums.tot[1][threadIdx.x];
   }
   if (!a.out) return;
-  if (r.W > 1) {
-    if (!exchange<NT>(r, h, xw, &late)) {
+  const double N = (double)a.P * a.cpg;
+  const auto group = [&](int g, double x, double y) {
+    g1[g] = (float)(x / N);
+    g2[g] = (float)(y / N);
+  };
+  if (r.W == 1) {
+    for (int g = threadIdx.x; g < r.Gb; g += NT)
+      group(g, word_lo(pieces.own[g]), word_hi(pieces.own[g]));
+    __syncthreads();
+  } else {
+    double s1 = 0.0, s2 = 0.0;
+    const auto sum = [&](int, unsigned long long x) {
+      s1 += (double)word_lo(x);
+      s2 += (double)word_hi(x);
+    };
+    if (!pieces.collect(r, h, sum)) {
+      s1 = s2 = 0.0;
       for (int w = 0; w < r.W; ++w) {
         long long fw;
         const int nw = rows_of(a, r, h, w, &fw);
@@ -658,30 +715,12 @@ __global__ __launch_bounds__(kGnResThreadsBwd, 2) void gn_resident_bwd_kernel(Gn
 #pragma unroll
           for (int j = 0; j < VEC; ++j) add(s, j, f[j], d[j]);
         }
-        piece(xw + w * r.Gb, s);
+        piece(s);
+        pieces.one(r, w, sum);
       }
     }
+    pieces.join(r, s1, s2, group);
   }
-  __syncthreads();
-  const double inv_n = 1.0 / ((double)a.P * a.cpg);
-  const double N = (double)a.P * a.cpg;
-  over_pieces<NT>(
-      r,
-      [&](int g, int lane, int lg) {
-        double s1 = 0.0, s2 = 0.0;
-        for (int w = lane; w < r.W; w += lg) {
-          s1 += (double)word_lo(xw[w * r.Gb + g]);
-          s2 += (double)word_hi(xw[w * r.Gb + g]);
-        }
-        return double2{lanes_sum(s1, lg), lanes_sum(s2, lg)};
-      },
-      [&](int g, int lane, double2 t) {
-        if (lane == 0) {
-          g1[g] = (float)(FEW ? t.x / N : t.x * inv_n);
-          g2[g] = (float)(FEW ? t.y / N : t.y * inv_n);
-        }
-      });
-  __syncthreads();
   if (!h.active) return;
   float c1[VEC], c2[VEC], gam[VEC];
   GroupOf go(gl0, a.cpg);
@@ -713,13 +752,25 @@ __global__ __launch_bounds__(kGnResThreadsBwd, 2) void gn_resident_bwd_kernel(Gn
       if (FEW) {
         vd[i].get(d);
         bv.run(f, d);
+      } else if (i < LROWS) {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 4) {
+          const f32x4_t q = lds_da[i][j / 4][threadIdx.x];
+          d[j] = q[0];
+          d[j + 1] = q[1];
+          d[j + 2] = q[2];
+          d[j + 3] = q[3];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) d[j] = vda[i - LROWS][j];
       }
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         if (FEW)
           f[j] = gn_dx(bv.rstd[bv.at(j)], gam[j], d[j], c1[j], f[j], c2[j]);
         else
-          f[j] = fmaf(vda[FEW ? 0 : i][j], gam[j],
+          f[j] = fmaf(d[j], gam[j],
                       fmaf(T::kWide ? bv.h(j, f[j]) : f[j], c2[j], c1[j]));
       }
       Held<T> o;
@@ -738,30 +789,36 @@ void clear_words(const GnTrainArgs& a, const GnResPlan& r, hipStream_t s) {
 template <class T, bool SILU>
 int run_fwd(const GnTrainArgs& a, const GnResPlan& r, hipStream_t s) {
   if (r.W > 1) clear_words(a, r, s);
-  const dim3 grid(a.units * r.NR * r.W);
-  const dim3 block(kGnResThreadsFwd);
+  const dim3 grid(a.units * r.NR * r.W), block(kGnResThreadsFwd);
   if (r.passes <= 4)
-    hipLaunchKernelGGL((gn_resident_fwd_kernel<T, SILU, 4>), grid, block, 0, s, a, r);
+    hipLaunchKernelGGL((gn_resident_fwd_kernel<T, SILU, 4, 0, false>), grid, block, 0, s, a, r);
+  else if (r.compact)
+    hipLaunchKernelGGL((gn_resident_fwd_kernel<T, SILU, kGnRowsFwdCompact, kGnRowsFwdLds, true>),
+                       grid, block, 0, s, a, r);
   else
-    hipLaunchKernelGGL((gn_resident_fwd_kernel<T, SILU, kGnResRowsFwd>), grid, block, 0, s, a, r);
+    hipLaunchKernelGGL((gn_resident_fwd_kernel<T, SILU, kGnRows, 0, false>), grid, block, 0, s, a,
+                       r);
   return (int)hipGetLastError();
 }
 
-template <class T, bool SILU, int R>
+template <class T, bool SILU, int R, int LROWS, bool COMPACT>
 void start_bwd(const GnTrainArgs& a, const GnResPlan& r, hipStream_t s) {
   constexpr int VEC = 16 / sizeof(typename T::store);
   const dim3 grid(a.units * r.NR * r.W), block(kGnResThreadsBwd);
   if (r.fold >= 4)
-    hipLaunchKernelGGL((gn_resident_bwd_kernel<T, SILU, R, VEC / 4>), grid, block, 0, s, a, r);
+    hipLaunchKernelGGL((gn_resident_bwd_kernel<T, SILU, R, LROWS, VEC / 4, COMPACT>), grid, block,
+                       0, s, a, r);
   else
-    hipLaunchKernelGGL((gn_resident_bwd_kernel<T, SILU, R, VEC>), grid, block, 0, s, a, r);
+    hipLaunchKernelGGL((gn_resident_bwd_kernel<T, SILU, R, LROWS, VEC, COMPACT>), grid, block, 0,
+                       s, a, r);
 }
 
 template <class T, bool SILU>
 int run_bwd(const GnTrainArgs& a, const GnResPlan& r, hipStream_t s) {
   if (r.W > 1 && a.out) clear_words(a, r, s);
-  if (r.passes <= 4) start_bwd<T, SILU, 4>(a, r, s);
-  else start_bwd<T, SILU, kGnResRowsBwd>(a, r, s);
+  if (r.passes <= 4) start_bwd<T, SILU, 4, 0, false>(a, r, s);
+  else if (r.compact) start_bwd<T, SILU, kGnRowsBwdCompact, kGnRowsBwdLds, true>(a, r, s);
+  else start_bwd<T, SILU, kGnRows, 0, false>(a, r, s);
   if (r.channel_sums)
     hipLaunchKernelGGL(column_sums_kernel, dim3((2 * a.C + kSumCols - 1) / kSumCols),
                        dim3(kSumThreads), 0, s, r.channel_sums, a.units * r.W, a.C, a.dgamma,

@@ -44,15 +44,19 @@ int launch_gn_train_bwd(const GnTrainArgs& args, void* stream);
 // (Cb channels in Vb 16-byte vectors), NR of them make C; the unit's pixels
 // are cut into W pieces of piece_px = ppi * passes.
 constexpr int kGnResThreadsFwd = 512, kGnResThreadsBwd = 256;
-constexpr int kGnResRowsFwd = 16, kGnResRowsBwd = 12;  // rows a thread can hold
-constexpr int kGnResWords = 4096;                      // words of one exchange
+// Rows a thread can hold: in registers alone, or in the compact form with
+// some of them in the LDS that it leaves free.
+constexpr int kGnRows = 12;
+constexpr int kGnRowsFwdCompact = 16, kGnRowsFwdLds = 6;
+constexpr int kGnRowsBwdCompact = 16, kGnRowsBwdLds = 7;
+constexpr int kGnCompact = 128;                        // values of a row in the compact form
 struct GnResPlan {
   int Cb, Vb, NR, Gb;
   int ppi, passes, piece_px, W;
   int lanes;                 // 1: a row is a power of two of lanes (at most a wave)
+  int compact;               // 1: lanes, and at most kGnCompact channels (backward) or slots
   int fold;                  // channels of a vector that always share a group (a power of two)
   int entry_lanes;           // lanes that join one group's rows of a piece (a power of two)
-  int join_lanes;            // lanes that join one group's pieces (a power of two)
   int spin;                  // polls of one word before a work-group helps itself
   unsigned long long* words; // [units][NR][W][Gb] (W > 1)
   float* channel_sums;       // backward: [units][W][2][C], or null

@@ -3,6 +3,7 @@
 // anything is enqueued.
 #include <math.h>
 #include <stdint.h>
+#include <stdlib.h>
 
 #include <algorithm>
 #include <initializer_list>
@@ -37,13 +38,22 @@ constexpr int kGnMaxPieces = 256;        // of one exchange; 512 work-groups are
 constexpr int kGnFill = 512;             // work-groups that fill the chip
 constexpr int kGnSpin = 20000;           // polls (about a microsecond each) before helping oneself
 
+// CONV3D_GN_SPIN: another bound, for tests (0: no work-group waits, each forms
+// the sums of its unit's other pieces itself).
+int spin_bound() {
+  const char* e = getenv("CONV3D_GN_SPIN");
+  if (!e) return kGnSpin;
+  const long v = strtol(e, nullptr, 10);
+  return (int)std::min(std::max(v, 0L), (long)kGnSpin);
+}
+
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
 // Ranges and pieces of the resident form for 16-byte vectors; false where a
 // unit's pieces are too many to be on the chip together.
 bool plan_resident(const GnTrainArgs& a, bool bwd, GnResPlan* r) {
   const int size = elt_size(a.dtype), vec = 16 / size;
-  const int rows = bwd ? kGnResRowsBwd : kGnResRowsFwd;
+  int rows = 0;                          // a thread can hold
   const int threads = bwd ? kGnResThreadsBwd : kGnResThreadsFwd;
   if (a.C % vec) return false;
   const int quantum = a.cpg / gcd(a.cpg, vec) * vec;    // whole groups in whole vectors
@@ -56,13 +66,13 @@ bool plan_resident(const GnTrainArgs& a, bool bwd, GnResPlan* r) {
     r->lanes = r->Vb <= 64 && (r->Vb & (r->Vb - 1)) == 0;
     r->fold = 1;
     while (r->fold < vec && a.cpg % (2 * r->fold) == 0) r->fold *= 2;
+    r->compact = r->lanes && (bwd ? Cb : Cb / r->fold) <= kGnCompact;
+    rows = !r->compact ? kGnRows : bwd ? kGnRowsBwdCompact : kGnRowsFwdCompact;
     const int entries = (r->lanes ? threads / 64 : r->ppi) * (a.cpg / r->fold);
     r->entry_lanes = 1;
     while (r->entry_lanes < 32 && 2 * r->entry_lanes <= entries &&
            2 * r->entry_lanes * r->Gb <= threads)
       r->entry_lanes *= 2;
-    r->join_lanes = 64;
-    while (r->join_lanes > 1 && r->join_lanes * r->Gb > threads) r->join_lanes /= 2;
   };
   const int limit = std::min(a.C, threads);
   // one work-group per range: the narrowest range of at least 64 bytes a pixel
@@ -90,7 +100,7 @@ bool plan_resident(const GnTrainArgs& a, bool bwd, GnResPlan* r) {
     r->passes = (int)((lanes + W - 1) / W);
     r->piece_px = r->ppi * r->passes;
     r->W = (int)((a.P + r->piece_px - 1) / r->piece_px);
-    return r->W * r->Gb <= kGnResWords && (long long)a.units * r->NR * r->W <= kGnMaxItems / 2 &&
+    return (long long)a.units * r->NR * r->W <= kGnMaxItems / 2 &&
            (long long)a.units * r->NR * r->W * r->Gb <= (1LL << 30);
   }
   return false;
@@ -144,7 +154,7 @@ conv3d_status plan_gn_train(const conv3d_group_norm_train_desc* d, bool bwd, GnT
   pl->total = (at + 255) / 256 * 256;
   // the resident form needs its words and channel sums instead
   pl->r = GnResPlan{};
-  pl->r.spin = kGnSpin;
+  pl->r.spin = spin_bound();
   pl->fits = plan_resident(a, bwd, &pl->r);
   if (pl->fits) {
     const GnResPlan& r = pl->r;

@@ -314,6 +314,44 @@ def test_two_streams_at_once():
         assert all(torch.equal(p, q) for p, q in zip(b, ref[i % 2]))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32], ids=str)
+@pytest.mark.parametrize("shape,groups", [((1, 2, 64, 65, 128), 32), ((1, 1, 61, 67, 96), 32),
+                                          ((2, 1, 48, 50, 320), 32), ((1, 1, 40, 41, 64), 1),
+                                          ((1, 2, 33, 31, 512), 16)])
+def test_pieces_that_help_themselves_agree_bit_for_bit(shape, groups, dtype, monkeypatch):
+    """Units of several pieces: with a bound of no polls at all every
+    work-group forms its unit's sums alone, and nothing changes."""
+    x, dy = (draw(shape, dtype, 90 + i).cuda() for i in range(2))
+    gamma, beta = (p.cuda() for p in params(shape[4], 92))
+    op = GroupNormTrain(shape, groups, silu=True, dtype=dtype)
+    y, stats = op.forward(x, gamma, beta)
+    want = (y, stats, *op.backward(dy, x, gamma, beta, stats))
+    torch.cuda.synchronize()
+    monkeypatch.setenv("CONV3D_GN_SPIN", "0")
+    y, stats = op.forward(x, gamma, beta)
+    got = (y, stats, *op.backward(dy, x, gamma, beta, stats))
+    torch.cuda.synchronize()
+    for a, b, what in zip(got, want, ("y", "stats", "dx", "dgamma", "dbeta")):
+        assert torch.equal(a, b), what
+
+
+BIG_SHAPES = [
+    # units of several pieces (exchanged), and units too large for that
+    ((1, 2, 128, 130, 128), 32, True, True), ((1, 1, 96, 100, 256), 32, False, True),
+    ((2, 3, 32, 40, 64), 8, True, False), ((1, 1, 100, 90, 96), 32, True, True),
+    ((1, 1, 64, 64, 480), 30, True, True), ((1, 1, 700, 720, 16), 4, True, True),
+    ((1, 1, 50, 60, 1024), 4, True, True),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("shape,groups,silu,t_iso", BIG_SHAPES)
+def test_group_norm_train_in_pieces(shape, groups, silu, t_iso, dtype):
+    """k: a thread adds at most 16 rows of a piece, or, in two passes, its
+    share of 504000 pixels in 2048 chunks."""
+    gn_case(shape, groups, dtype, silu, t_iso, seed=sum(shape))
+
+
 # ------------------------------------------------------- channel norm + SiLU
 
 def ns_case(shape, *, skip=False, bias=True, value=None, seed=0):
