@@ -34,122 +34,151 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-template <int G, int K, bool SUMS>
+// DB: dbias is wanted too; without it the registers of its sums are free.
+template <int G, int K, bool DG, bool DB>
 __global__ __launch_bounds__(kThreads) void ns_bwd_kernel(NsBwdArgs a) {
-  typedef Pack<Bf16, 8> V8;
+  constexpr bool SUMS = DG || DB;
   __shared__ float sums[SUMS ? kThreads / G : 1][SUMS ? G * 8 : 1];
   const int gl = threadIdx.x % G, row0 = threadIdx.x / G;
   const int V = a.C / 8;
-  const float root = sqrtf((float)a.C);
-  float gamma[K][8], dg[K][8], db[K][8];
+  const float root = sqrtf((float)a.C), inv_c = 1.0f / (float)a.C;
+  Held<Bf16> gamma[K];
+  float dg[DG ? K : 1][8], db[DB ? K : 1][8];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int cv = gl + k * G;
-    if (cv < V) {
-      unpack<Bf16, 8>(((const V8*)a.gamma)[cv], gamma[k]);
-    } else {
+    gamma[k].v = u32x4_t{0, 0, 0, 0};
+    if (gl + k * G < V) gamma[k].v = ((const u32x4_t*)a.gamma)[gl + k * G];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) gamma[k][j] = 0.0f;
+    for (int j = 0; j < 8; ++j) {
+      if (DG) dg[k][j] = 0.0f;
+      if (DB) db[k][j] = 0.0f;
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dg[k][j] = db[k][j] = 0.0f;
   }
   const long long step = (long long)gridDim.x * (kThreads / G);
-  for (long long r = (long long)blockIdx.x * (kThreads / G) + row0; r < a.M; r += step) {
-    const long long at = r * V + gl;
-    V8 pv[K], pd[K], ps[K];
+  long long r = (long long)blockIdx.x * (kThreads / G) + row0;
+  Held<Bf16> v[K], d[K];
+  const auto load = [&](long long row) {
+    const long long at = row * V + gl;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
+      v[k].v = d[k].v = u32x4_t{0, 0, 0, 0};
       if (gl + k * G < V) {
-        pv[k] = ((const V8*)a.value)[at + k * G];
-        pd[k] = ((const V8*)a.dy)[at + k * G];
-        if (a.dskip) ps[k] = ((const V8*)a.dskip)[at + k * G];
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) pv[k].v[j] = pd[k].v[j] = 0;
+        v[k].v = ((const u32x4_t*)a.value)[at + k * G];
+        d[k].v = ((const u32x4_t*)a.dy)[at + k * G];
       }
     }
-    float v[K][8], g[K][8], n2 = 0.0f;
+  };
+  if (r < a.M) load(r);
+  for (; r < a.M; r += step) {
+    const long long at = r * V + gl;
+    Held<Bf16> sk[K];
+    if (a.dskip) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (gl + k * G < V) sk[k].v = ((const u32x4_t*)a.dskip)[at + k * G];
+    }
+    float n2 = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      unpack<Bf16, 8>(pv[k], v[k]);
+      float x[8];
+      v[k].get(x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) n2 = fmaf(v[k][j], v[k][j], n2);
+      for (int j = 0; j < 8; ++j) n2 = fmaf(x[j], x[j], n2);
     }
     n2 = group_sum<G>(n2);
     const float norm = sqrtf(n2);
     const bool clamped = norm <= 1e-12f;             // and not fmaxf: a NaN stays
     const float s = root / (clamped ? 1e-12f : norm);
-    float dot = 0.0f;
+    float g[K][8], dot = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      float d[8];
-      unpack<Bf16, 8>(pd[k], d);
+      // a vector's values step by step, so that no exponential or reciprocal
+      // is waited for alone
+      constexpr float kLog2e = 1.44269502162933349609375f;
+      float e[8], gm[8], t[8], dy[8];
+      v[k].get(e);
+      gamma[k].get(gm);
+      d[k].get(dy);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float e = v[k][j] * s, act = e * gamma[k][j];
-        const float da = d[j] * silu_slope<false>(act);
-        if (SUMS) dg[k][j] = fmaf(da, e, dg[k][j]);
-        g[k][j] = da * gamma[k][j];
-        dot = fmaf(g[k][j], e, dot);
+        e[j] *= s;
+        g[k][j] = e[j] * gm[j];
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] = __builtin_amdgcn_exp2f(g[k][j] * -kLog2e);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] = __builtin_amdgcn_rcpf(1.0f + t[j]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float da = dy[j] * (t[j] * fmaf(g[k][j], 1.0f - t[j], 1.0f));
+        if (DG) dg[k][j] = fmaf(da, e[j], dg[k][j]);
+        g[k][j] = da * gm[j];
+        dot = fmaf(g[k][j], e[j], dot);
       }
     }
     // g v / |v|^2 with g and v scaled: (g s)(v s) / (s |v|)^2, and s |v| = root
     dot = group_sum<G>(dot);
-    const float back = clamped ? 0.0f : dot / (float)a.C;
+    const float back = clamped ? 0.0f : dot * inv_c * s;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (gl + k * G >= V) continue;
-      float o[8], sk[8];
-      if (a.dskip) unpack<Bf16, 8>(ps[k], sk);
+      float o[8], x[8], y[8];
+      v[k].get(x);
+      if (a.dskip) sk[k].get(y);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        o[j] = s * (g[k][j] - v[k][j] * s * back);
-        if (a.dskip) o[j] += sk[j];
-        if (SUMS) db[k][j] += o[j];
+        o[j] = s * fmaf(-x[j], back, g[k][j]);
+        if (a.dskip) o[j] += y[j];
+        if (DB) db[k][j] += o[j];
       }
-      ((V8*)a.dvalue)[at + k * G] = pack<Bf16, 8>(o);
+      Held<Bf16> out;
+      out.put(o);
+      if (gl + k * G < V) ((u32x4_t*)a.dvalue)[at + k * G] = out.v;
     }
+    if (r + step < a.M) load(r + step);
   }
   if (SUMS) {
     float* out = a.partial + (long long)blockIdx.x * 2 * a.C;
 #pragma unroll
-    for (int which = 0; which < 2; ++which)
+    for (int which = 0; which < 2; ++which) {
+      if (which ? !DB : !DG) continue;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sums[row0][gl * 8 + j] = which ? db[k][j] : dg[k][j];
+        for (int j = 0; j < 8; ++j)
+          sums[row0][gl * 8 + j] = which ? db[DB ? k : 0][j] : dg[DG ? k : 0][j];
         __syncthreads();
-        const int c = k * G * 8 + threadIdx.x;
-        if (threadIdx.x < G * 8 && c < a.C) {
+        for (int i = threadIdx.x; i < G * 8 && k * G * 8 + i < a.C; i += kThreads) {
           float t = 0.0f;
-          for (int i = 0; i < kThreads / G; ++i) t += sums[i][threadIdx.x];
-          out[which * a.C + c] = t;
-        }
-        if (G * 8 > kThreads && threadIdx.x + kThreads < G * 8 && c + kThreads < a.C) {
-          float t = 0.0f;
-          for (int i = 0; i < kThreads / G; ++i) t += sums[i][threadIdx.x + kThreads];
-          out[which * a.C + c + kThreads] = t;
+          for (int q = 0; q < kThreads / G; ++q) t += sums[q][i];
+          out[which * a.C + k * G * 8 + i] = t;
         }
       }
+    }
   }
 }
 
 template <int G, int K>
 void launch(const NsBwdArgs& a, hipStream_t s) {
-  if (a.dgamma || a.dbias)
-    hipLaunchKernelGGL((ns_bwd_kernel<G, K, true>), dim3(a.blocks), dim3(kThreads), 0, s, a);
+  const dim3 grid(a.blocks), block(kThreads);
+  if (a.dbias)
+    hipLaunchKernelGGL((ns_bwd_kernel<G, K, true, true>), grid, block, 0, s, a);
+  else if (a.dgamma)
+    hipLaunchKernelGGL((ns_bwd_kernel<G, K, true, false>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((ns_bwd_kernel<G, K, false>), dim3(a.blocks), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((ns_bwd_kernel<G, K, false, false>), grid, block, 0, s, a);
 }
 
-// Lanes that share a row: the fewest (a power of two) whose K <= 4 vectors
-// each cover it.
+// Lanes that share a row: the fewest (a power of two, at most a wave) whose
+// three vectors each cover it; four only for the widest rows (their registers
+// leave one wave per SIMD).
 int lanes_per_row(int C) {
   const int V = C / 8;
   int g = 1;
-  while (g * 4 < V) g *= 2;
+  while (g < 64 && g * 3 < V) g *= 2;
   return g;
 }
 

@@ -35,7 +35,7 @@ struct GnTrainPlan {
 };
 
 constexpr int kGnMaxPieces = 256;        // of one exchange; 512 work-groups are resident
-constexpr int kGnFill = 512;             // work-groups that fill the chip
+constexpr int kGnFill = 256;             // work-groups that give every CU one
 constexpr int kGnSpin = 20000;           // polls (about a microsecond each) before helping oneself
 
 // CONV3D_GN_SPIN: another bound, for tests (0: no work-group waits, each forms
@@ -413,17 +413,25 @@ conv3d_status plan_grads(const conv3d_grad* g, int count, GradPlan* pl) {
 
 struct Span {
   uintptr_t lo, hi;
-  bool write;
 };
 
+// By address; lists that come in that order already, as most do, are not sorted.
+void by_address(std::vector<Span>& v) {
+  const auto less = [](const Span& a, const Span& b) { return a.lo < b.lo; };
+  if (!std::is_sorted(v.begin(), v.end(), less)) std::sort(v.begin(), v.end(), less);
+}
+
 // Every written range must lie apart from every other range.
-bool spans_clash(std::vector<Span>& v) {
-  std::sort(v.begin(), v.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
-  uintptr_t any = 0, written = 0;
-  for (const Span& s : v) {
-    if (s.lo < (s.write ? any : written)) return true;
-    any = std::max(any, s.hi);
-    if (s.write) written = std::max(written, s.hi);
+bool spans_clash(std::vector<Span>& reads, std::vector<Span>& writes) {
+  by_address(reads);
+  by_address(writes);
+  size_t i = 0;
+  uintptr_t read_to = 0;                 // the end of all reads that begin below w.hi
+  for (size_t k = 0; k < writes.size(); ++k) {
+    const Span& w = writes[k];
+    if (k && w.lo < writes[k - 1].hi) return true;
+    for (; i < reads.size() && reads[i].lo < w.hi; ++i) read_to = std::max(read_to, reads[i].hi);
+    if (read_to > w.lo) return true;
   }
   return false;
 }
@@ -437,8 +445,9 @@ conv3d_status run_grads(const conv3d_grad* g, int count, int norm_type, bool cli
   GradPlan pl;
   conv3d_status st = plan_grads(g, count, &pl);
   if (st != CONV3D_OK) return st;
-  std::vector<Span> spans;
-  spans.reserve((size_t)count * 2 + 2);
+  std::vector<Span> reads, writes;
+  reads.reserve((size_t)count);
+  writes.reserve((size_t)count + 2);
   int last = -1;                         // the last tensor that holds anything
   for (int i = 0; i < count; ++i) {
     if (g[i].numel == 0) continue;
@@ -448,19 +457,20 @@ conv3d_status run_grads(const conv3d_grad* g, int count, int norm_type, bool cli
     if (src % (unsigned)elt_size(g[i].dtype)) return CONV3D_ERR_ALIGN;
     const bool in_place = !g[i].out || g[i].out == g[i].grad;
     if (clip && in_place && g[i].out_dtype != g[i].dtype) return CONV3D_ERR_OVERLAP;
-    spans.push_back({src, src + (uintptr_t)g[i].numel * elt_size(g[i].dtype), clip && in_place});
+    (clip && in_place ? writes : reads)
+        .push_back({src, src + (uintptr_t)g[i].numel * elt_size(g[i].dtype)});
     if (clip && !in_place) {
       const uintptr_t dst = (uintptr_t)g[i].out;
       if (dst % (unsigned)elt_size(g[i].out_dtype)) return CONV3D_ERR_ALIGN;
-      spans.push_back({dst, dst + (uintptr_t)g[i].numel * elt_size(g[i].out_dtype), true});
+      writes.push_back({dst, dst + (uintptr_t)g[i].numel * elt_size(g[i].out_dtype)});
     }
   }
   if (!aligned_to(norm, 4)) return CONV3D_ERR_ALIGN;
   if (!workspace || workspace_bytes < pl.bytes) return CONV3D_ERR_WORKSPACE;
   if (!aligned16(workspace)) return CONV3D_ERR_ALIGN;
-  spans.push_back({(uintptr_t)norm, (uintptr_t)norm + 4, true});
-  spans.push_back({(uintptr_t)workspace, (uintptr_t)workspace + pl.bytes, true});
-  if (spans_clash(spans)) return CONV3D_ERR_OVERLAP;
+  writes.push_back({(uintptr_t)norm, (uintptr_t)norm + 4});
+  writes.push_back({(uintptr_t)workspace, (uintptr_t)workspace + pl.bytes});
+  if (spans_clash(reads, writes)) return CONV3D_ERR_OVERLAP;
 
   double* partial = (double*)workspace;
   GradBatch b{};
