@@ -135,7 +135,9 @@ __device__ __forceinline__ void scale_range(const void* src, void* dst, long lon
                                             float coef) {
   typedef typename T::store E;
   typedef typename O::store F;
-  constexpr int VEC = 16 / sizeof(E), U = 4;
+  // 16 bytes of the wider type per lane, so that a wave's loads and stores are
+  // both without gaps
+  constexpr int VEC = 16 / (sizeof(E) > sizeof(F) ? sizeof(E) : sizeof(F)), U = 8;
   typedef Loose<T, VEC> L;
   typedef Loose<O, VEC> S;
   const E* p = (const E*)src + at;

@@ -313,13 +313,14 @@ class GroupNormTrain:
         _vector(gamma, self.c, torch.float32, dev, "gamma")
         _vector(beta, self.c, torch.float32, dev, "beta")
         if y is None:
-            y = torch.empty(self.x_shape, dtype=self.dtype, device=dev)
+            y, yp = torch.empty(self.x_shape, dtype=self.dtype, device=dev), self.c
+        else:
+            yp = _activation(y, self.x_shape, self.dtype, "y")
+            _same_device(dev, y=y)
         if stats is None:
             stats = torch.empty(self.stats_shape, dtype=torch.float32, device=dev)
         else:
             _vector(stats, self._stats_numel, torch.float32, dev, "stats")
-        yp = _activation(y, self.x_shape, self.dtype, "y")
-        _same_device(dev, y=y)
         ws = torch.empty(self._ws[0], dtype=torch.uint8, device=dev)
         conv3d_group_norm_train_fwd(self._desc(xp, yp, yp), x, gamma, beta, y, stats, ws,
                                     self._ws[0], _current_stream(dev.index))
@@ -340,14 +341,13 @@ class GroupNormTrain:
         _vector(gamma, self.c, torch.float32, dev, "gamma")
         _vector(beta, self.c, torch.float32, dev, "beta")
         _vector(stats, self._stats_numel, torch.float32, dev, "stats")
-        if not need_dx:
-            if dx is not None:
+        op = self.c
+        if dx is not None:
+            if not need_dx:
                 raise ValueError("dx is given but not wanted")
-            op = self.c
-        else:
-            if dx is None:
-                dx = torch.empty(self.x_shape, dtype=self.dtype, device=dev)
             op = _activation(dx, self.x_shape, self.dtype, "dx")
+        elif need_dx:
+            dx = torch.empty(self.x_shape, dtype=self.dtype, device=dev)
         _same_device(dev, dy=dy, dx=dx)
         dgamma = dbeta = None
         if need_params:
@@ -380,7 +380,6 @@ class NormSiluBackward:
         _expect(value, self.x_shape, "value")
         _expect(dy, self.x_shape, "dy")
         _expect(dskip, self.x_shape, "dskip")
-        _expect(dvalue, self.x_shape, "dvalue")
         _same_device(dev, dy=dy, dskip=dskip, dvalue=dvalue)
         if dev.index != torch.cuda.current_device():
             with torch.cuda.device(dev):
@@ -389,6 +388,8 @@ class NormSiluBackward:
         _vector(gamma, c, torch.bfloat16, dev, "gamma")
         if dvalue is None:
             dvalue = torch.empty_like(value)
+        else:
+            _expect(dvalue, self.x_shape, "dvalue")
         dgamma = torch.empty(c, dtype=torch.float32, device=dev) if self.want_gamma else None
         dbias = torch.empty(c, dtype=torch.float32, device=dev) if self.want_bias else None
         ws = None
