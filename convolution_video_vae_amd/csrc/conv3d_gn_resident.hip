@@ -1,10 +1,10 @@
 // Training GroupNorm (formulas in conv3d_gn_train.hip) that reads its
 // activations once.
 //
-// A work-group keeps a piece of a unit in registers: some
-// pixels of some whole groups' channels (a range). It forms the piece's
-// sums, and once the sums of the whole unit are known it computes the result
-// from the registers. Where a range's pixels fit one work-group (W = 1) no
+// A work-group keeps a piece of a unit in registers and LDS: some pixels of
+// some whole groups' channels (a range). It forms the piece's sums, and once
+// the sums of the whole unit are known it computes the result from what it
+// holds. Where a range's pixels fit one work-group (W = 1) no
 // other work-group is involved. Otherwise the W pieces of a (unit, range)
 // exchange their sums while all of them are on the chip: HBM then carries
 // x + y instead of 2 x + y, and x + dy + dx instead of 2 x + 2 dy + dx.
@@ -21,8 +21,8 @@
 // against it and no cache is written back (a release per work-group would
 // write back its XCD's L2).
 //
-// Every wait ends. A work-group polls each word at most `spin` times; if a
-// word is still empty then (the other pieces cannot be resident at the same
+// Every wait ends. A thread polls at most `spin` times for all its words
+// together; if one is still empty then (the other pieces cannot be resident at the same
 // time: a stream confined to few CUs, other kernels that hold the chip), it
 // loads the unit's other pieces itself, forms their sums with the same code
 // and in the same order, and goes on. Results are therefore the same, bit
@@ -302,11 +302,12 @@ struct PieceSums {
     const int LG = NT / r.Gb, slot = t / r.Gb, g = t - slot * r.Gb;
     // two words in flight per thread: a poll is a trip to memory, behind the
     // rows that the other work-group on this CU has asked for
+    int left = r.spin;
     for (int w0 = slot < LG ? slot : r.W; w0 < r.W; w0 += 2 * LG) {
       const int w1 = w0 + LG;
       bool open0 = w0 != h.w, open1 = w1 < r.W && w1 != h.w;
       unsigned long long v0 = own[g], v1 = v0;
-      for (int k = 0; k < r.spin && (open0 | open1); ++k) {
+      for (; left > 0 && (open0 | open1); --left) {
         if (open0)
           v0 = __hip_atomic_load(words + w0 * r.Gb + g, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         if (open1)

@@ -57,7 +57,7 @@ struct GnResPlan {
   int compact;               // 1: lanes, and at most kGnCompact channels (backward) or slots
   int fold;                  // channels of a vector that always share a group (a power of two)
   int entry_lanes;           // lanes that join one group's rows of a piece (a power of two)
-  int spin;                  // polls of one word before a work-group helps itself
+  int spin;                  // polls of a thread before its work-group helps itself
   unsigned long long* words; // [units][NR][W][Gb] (W > 1)
   float* channel_sums;       // backward: [units][W][2][C], or null
 };

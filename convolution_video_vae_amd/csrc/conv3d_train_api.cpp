@@ -36,7 +36,7 @@ struct GnTrainPlan {
 
 constexpr int kGnMaxPieces = 256;        // of one exchange; 512 work-groups are resident
 constexpr int kGnFill = 256;             // work-groups that give every CU one
-constexpr int kGnSpin = 20000;           // polls (about a microsecond each) before helping oneself
+constexpr int kGnSpin = 20000;           // polls (some 20 ms) before a work-group helps itself
 
 // CONV3D_GN_SPIN: another bound, for tests (0: no work-group waits, each forms
 // the sums of its unit's other pieces itself).

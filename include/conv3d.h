@@ -384,7 +384,9 @@ conv3d_status conv3d_group_norm_from_partials(const conv3d_group_norm_desc* desc
  *   dgamma[c] = sum over all pixels of da * h, dbeta[c] = of da
  * A NaN or an infinity makes its own unit and group (and in dgamma, dbeta its
  * channels) NaN. Differences from the mean beyond 2^63 overflow the sum of
- * squares. Results do not change from call to call (no atomics). */
+ * squares. The same call gives the same bits every time. A workspace serves
+ * one call at a time: calls that may overlap in time (other streams, graphs
+ * replayed side by side) need their own, here and in the calls below. */
 typedef enum { CONV3D_ELT_BF16 = 0, CONV3D_ELT_FP16 = 1, CONV3D_ELT_FP32 = 2 } conv3d_elt;
 
 typedef struct {

@@ -189,13 +189,30 @@ def test_dx_in_place_of_dy_and_gradients_left_out():
     assert same is dy and torch.equal(dy, dx) and torch.equal(a, dg)
 
 
-def test_nothing_outside_the_outputs_is_written():
-    shape = (1, 2, 7, 5, 40)
+def test_dx_in_place_of_dy_in_units_of_several_pieces():
+    shape = (1, 2, 64, 65, 128)
+    x, dy = draw(shape, torch.bfloat16, 93), draw(shape, torch.bfloat16, 94)
+    gamma, beta = params(128, 95)
+    op = GroupNormTrain(shape, 32, silu=True)
+    _, stats = op.forward(x.cuda(), gamma.cuda(), beta.cuda())
+    dyd = dy.cuda()
+    dx, dg, db = op.backward(dyd, x.cuda(), gamma.cuda(), beta.cuda(), stats, dx=dyd)
+    (rx, rg, rb), (tx, tg, tb) = train.group_norm_bwd(np64(dy), np64(x), 32, np64(gamma),
+                                                      np64(beta), np64(stats), silu=True,
+                                                      t_isolated=True)
+    check(dx, rx, tx, "dx")
+    check(dg, rg, tg, "dgamma")
+    check(db, rb, tb, "dbeta")
+
+
+@pytest.mark.parametrize("shape", [(1, 2, 7, 5, 40), (1, 1, 67, 61, 64)])
+def test_nothing_outside_the_outputs_is_written(shape):
+    c = shape[4]
     bufs = {k: Guarded(shape) for k in ("y", "dx")}
-    small = {k: Guarded((40,), torch.float32) for k in ("dg", "db")}
-    stats = Guarded((2, 8, 2), torch.float32)
+    small = {k: Guarded((c,), torch.float32) for k in ("dg", "db")}
+    stats = Guarded((shape[1], 8, 2), torch.float32)
     x, dy = draw(shape, torch.bfloat16, 15).cuda(), draw(shape, torch.bfloat16, 16).cuda()
-    gamma, beta = (p.cuda() for p in params(40, 17))
+    gamma, beta = (p.cuda() for p in params(c, 17))
     d = cv.make_group_norm_train_desc(shape, 8, silu=True)
     n = [cv.conv3d_group_norm_train_workspace_bytes(d, b) for b in (False, True)]
     ws = [Guarded((v // 2,), torch.int16) for v in n]
