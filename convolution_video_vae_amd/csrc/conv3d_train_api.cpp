@@ -34,8 +34,16 @@ struct GnTrainPlan {
   size_t off_sums;
 };
 
-constexpr int kGnMaxPieces = 256;        // of one exchange; 512 work-groups are resident
+// Pieces of one exchange: half of the 512 work-groups that the chip holds, so
+// that two calls side by side still find room. (Resident against two passes,
+// backward: [1,8,256,512,128] bf16, 256 pieces, 222 and 278 us; at 384 pieces
+// 192 and 218 us, left to two passes for that room.)
+constexpr int kGnMaxPieces = 256;
 constexpr int kGnFill = 256;             // work-groups that give every CU one
+// Rows per thread up to which one work-group per narrow range is better than
+// an exchange, where the chip is not filled ([1,5,32,32,512] bf16 forward, 8
+// rows: 10.0 and 11.2 us; backward, 16 rows: 21.7 and 17.5 us).
+constexpr int kGnAloneRows = 10;
 constexpr int kGnSpin = 20000;           // polls (some 20 ms) before a work-group helps itself
 
 // CONV3D_GN_SPIN: another bound, for tests (0: no work-group waits, each forms
@@ -75,17 +83,18 @@ bool plan_resident(const GnTrainArgs& a, bool bwd, GnResPlan* r) {
       r->entry_lanes *= 2;
   };
   const int limit = std::min(a.C, threads);
-  // one work-group per range: the narrowest range of at least 64 bytes a pixel
+  // few units: one work-group per range, the narrowest of at least 64 bytes a
+  // pixel. (Where such ranges fill the chip, half lines cost more than an
+  // exchange: [8,5,32,32,512] bf16 forward 39.5 us, as below 26.7 us.)
   for (int Cb = quantum; Cb <= limit; Cb += quantum) {
     if (a.C % Cb || (Cb * size < 64 && Cb < a.C)) continue;
     lay(Cb);
-    r->passes = (int)std::min((a.P + r->ppi - 1) / r->ppi, (long long)rows + 1);
-    if (r->passes <= rows) {
-      r->W = 1;
-      r->piece_px = r->ppi * r->passes;
-      return (long long)a.units * r->NR <= kGnMaxItems / 2;   // 512 threads each
-    }
-    break;
+    const long long passes = (a.P + r->ppi - 1) / r->ppi;
+    if (passes > kGnAloneRows || (long long)a.units * r->NR > kGnFill) break;
+    r->passes = (int)passes;
+    r->W = 1;
+    r->piece_px = r->ppi * r->passes;
+    return true;
   }
   // pieces: whole 128-byte lines, as few pieces as hold the unit, but enough
   // work-groups to fill the chip
