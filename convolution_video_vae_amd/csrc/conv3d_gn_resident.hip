@@ -11,8 +11,9 @@
 //
 // Rows are loaded as non-temporal: they are read once, and what they would
 // push out of the memory-side cache are dirty lines of y or dx, whose
-// write-back then competes with the loads (H3 L0 forward 134 -> 120 us,
-// backward 223 -> 203 us).
+// write-back then competes with the loads (H3 L0 forward 134 -> 128 us,
+// backward 218 -> 209 us). So are results stored that would fill half of that
+// cache and more (121 and 205 us); smaller ones stay there for their reader.
 //
 // The exchange. Each piece publishes one 64-bit word per group (two fp32
 // sums) with a relaxed agent-scope atomic store, and reads the others' words
@@ -63,6 +64,14 @@ __global__ __launch_bounds__(256) void gn_words_clear_kernel(unsigned long long*
 __device__ __forceinline__ float mul_alone(float a, float b) {
 #pragma clang fp contract(off)
   return a * b;
+}
+
+// STREAM is a template argument: the compiler joins the two stores of a branch
+// into an ordinary one.
+template <bool STREAM>
+__device__ __forceinline__ void store_row(void* p, const u32x4_t& v) {
+  if (STREAM) __builtin_nontemporal_store(v, (u32x4_t*)p);
+  else *(u32x4_t*)p = v;
 }
 
 // What a thread of a work-group holds: rows first + i * ppi, i < n, of vector
@@ -371,7 +380,7 @@ struct PieceSums {
 __device__ __forceinline__ void step_edge() { __builtin_amdgcn_sched_barrier(0); }
 
 // R rows of which LROWS are kept in LDS.
-template <class T, bool SILU, int R, int LROWS, bool COMPACT>
+template <class T, bool SILU, int R, int LROWS, bool COMPACT, bool STREAM>
 __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(GnTrainArgs a,
                                                                               GnResPlan r) {
   typedef typename T::store E;
@@ -535,7 +544,7 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
       }
       Held<T> o;
       o.put(f);
-      *(u32x4_t*)y = o.v;
+      store_row<STREAM>(y, o.v);
     }
     y += step;
   }
@@ -597,7 +606,7 @@ struct BwdValues {
 // formed again. More rows: da is kept in the place of dy, of LROWS rows in LDS,
 // and dx is two products per value. GV groups at most share a vector's channels: VEC, or
 // a quarter of that where every four channels are of one group.
-template <class T, bool SILU, int R, int LROWS, int GV, bool COMPACT>
+template <class T, bool SILU, int R, int LROWS, int GV, bool COMPACT, bool STREAM>
 __global__ __launch_bounds__(kGnResThreadsBwd, 2) void gn_resident_bwd_kernel(GnTrainArgs a,
                                                                               GnResPlan r) {
   typedef typename T::store E;
@@ -781,7 +790,7 @@ __global__ __launch_bounds__(kGnResThreadsBwd, 2) void gn_resident_bwd_kernel(Gn
       }
       Held<T> o;
       o.put(f);
-      *(u32x4_t*)dx = o.v;
+      store_row<STREAM>(dx, o.v);
     }
     dx += step;
   }
@@ -796,35 +805,42 @@ template <class T, bool SILU>
 int run_fwd(const GnTrainArgs& a, const GnResPlan& r, hipStream_t s) {
   if (r.W > 1) clear_words(a, r, s);
   const dim3 grid(a.units * r.NR * r.W), block(kGnResThreadsFwd);
+  constexpr int R = kGnRowsFwdCompact, L = kGnRowsFwdLds;
   if (r.passes <= 4)
-    hipLaunchKernelGGL((gn_resident_fwd_kernel<T, SILU, 4, 0, false>), grid, block, 0, s, a, r);
-  else if (r.compact)
-    hipLaunchKernelGGL((gn_resident_fwd_kernel<T, SILU, kGnRowsFwdCompact, kGnRowsFwdLds, true>),
-                       grid, block, 0, s, a, r);
-  else
-    hipLaunchKernelGGL((gn_resident_fwd_kernel<T, SILU, kGnRows, 0, false>), grid, block, 0, s, a,
+    hipLaunchKernelGGL((gn_resident_fwd_kernel<T, SILU, 4, 0, false, false>), grid, block, 0, s, a,
                        r);
+  else if (r.compact && r.stream)
+    hipLaunchKernelGGL((gn_resident_fwd_kernel<T, SILU, R, L, true, true>), grid, block, 0, s, a,
+                       r);
+  else if (r.compact)
+    hipLaunchKernelGGL((gn_resident_fwd_kernel<T, SILU, R, L, true, false>), grid, block, 0, s, a,
+                       r);
+  else
+    hipLaunchKernelGGL((gn_resident_fwd_kernel<T, SILU, kGnRows, 0, false, false>), grid, block, 0,
+                       s, a, r);
   return (int)hipGetLastError();
 }
 
-template <class T, bool SILU, int R, int LROWS, bool COMPACT>
+template <class T, bool SILU, int R, int LROWS, bool COMPACT, bool STREAM>
 void start_bwd(const GnTrainArgs& a, const GnResPlan& r, hipStream_t s) {
   constexpr int VEC = 16 / sizeof(typename T::store);
   const dim3 grid(a.units * r.NR * r.W), block(kGnResThreadsBwd);
   if (r.fold >= 4)
-    hipLaunchKernelGGL((gn_resident_bwd_kernel<T, SILU, R, LROWS, VEC / 4, COMPACT>), grid, block,
-                       0, s, a, r);
+    hipLaunchKernelGGL((gn_resident_bwd_kernel<T, SILU, R, LROWS, VEC / 4, COMPACT, STREAM>), grid,
+                       block, 0, s, a, r);
   else
-    hipLaunchKernelGGL((gn_resident_bwd_kernel<T, SILU, R, LROWS, VEC, COMPACT>), grid, block, 0,
-                       s, a, r);
+    hipLaunchKernelGGL((gn_resident_bwd_kernel<T, SILU, R, LROWS, VEC, COMPACT, STREAM>), grid,
+                       block, 0, s, a, r);
 }
 
 template <class T, bool SILU>
 int run_bwd(const GnTrainArgs& a, const GnResPlan& r, hipStream_t s) {
   if (r.W > 1 && a.out) clear_words(a, r, s);
-  if (r.passes <= 4) start_bwd<T, SILU, 4, 0, false>(a, r, s);
-  else if (r.compact) start_bwd<T, SILU, kGnRowsBwdCompact, kGnRowsBwdLds, true>(a, r, s);
-  else start_bwd<T, SILU, kGnRows, 0, false>(a, r, s);
+  constexpr int R = kGnRowsBwdCompact, L = kGnRowsBwdLds;
+  if (r.passes <= 4) start_bwd<T, SILU, 4, 0, false, false>(a, r, s);
+  else if (r.compact && r.stream) start_bwd<T, SILU, R, L, true, true>(a, r, s);
+  else if (r.compact) start_bwd<T, SILU, R, L, true, false>(a, r, s);
+  else start_bwd<T, SILU, kGnRows, 0, false, false>(a, r, s);
   if (r.channel_sums)
     hipLaunchKernelGGL(column_sums_kernel, dim3((2 * a.C + kSumCols - 1) / kSumCols),
                        dim3(kSumThreads), 0, s, r.channel_sums, a.units * r.W, a.C, a.dgamma,

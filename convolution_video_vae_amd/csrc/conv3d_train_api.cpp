@@ -40,6 +40,7 @@ struct GnTrainPlan {
 // 192 and 218 us, left to two passes for that room.)
 constexpr int kGnMaxPieces = 256;
 constexpr int kGnFill = 256;             // work-groups that give every CU one
+constexpr long long kGnStreamBytes = 128LL << 20;    // half of the memory-side cache
 // Rows per thread up to which one work-group per narrow range is better than
 // an exchange, where the chip is not filled ([1,5,32,32,512] bf16 forward, 8
 // rows: 10.0 and 11.2 us; backward, 16 rows: 21.7 and 17.5 us).
@@ -164,6 +165,7 @@ conv3d_status plan_gn_train(const conv3d_group_norm_train_desc* d, bool bwd, GnT
   // the resident form needs its words and channel sums instead
   pl->r = GnResPlan{};
   pl->r.spin = spin_bound();
+  pl->r.stream = prod({units, P, a.C, size}) > kGnStreamBytes;
   pl->fits = plan_resident(a, bwd, &pl->r);
   if (pl->fits) {
     const GnResPlan& r = pl->r;

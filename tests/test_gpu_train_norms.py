@@ -245,6 +245,37 @@ def test_gradient_against_differences():
     assert abs(slope - mine) < 1e-3 * scale
 
 
+def test_full_size_activation():
+    """[1,17,256,256,128] bf16, whose results are stored past the caches: the
+    first and last frames against the reference, the parameters' gradients
+    against the sum of the frames' own."""
+    shape = (1, 17, 256, 256, 128)
+    g = torch.Generator(device="cuda").manual_seed(96)
+    x = torch.randn(shape, generator=g, device="cuda").bfloat16()
+    dy = (torch.randn(shape, generator=g, device="cuda") * 0.1).bfloat16()
+    gamma, beta = params(128, 97)
+    op = GroupNormTrain(shape, 32, silu=True)
+    one = GroupNormTrain((1, 1) + shape[2:], 32, silu=True)
+    y, stats = op.forward(x, gamma.cuda(), beta.cuda())
+    dx, dg, db = op.backward(dy, x, gamma.cuda(), beta.cuda(), stats)
+    kw = dict(silu=True, t_isolated=True)
+    for f in (0, 16):
+        at = slice(f, f + 1)
+        ry, _, ty = train.group_norm_fwd(np64(x[:, at]), 32, np64(gamma), np64(beta),
+                                         eps=float(np.float32(EPS)), **kw)
+        check(y[:, at], ry, ty, f"y of frame {f}")
+        (rx, _, _), (tx, _, _) = train.group_norm_bwd(np64(dy[:, at]), np64(x[:, at]), 32,
+                                                      np64(gamma), np64(beta), np64(stats[at]), **kw)
+        check(dx[:, at], rx, tx, f"dx of frame {f}")
+    each = [one.backward(dy[:, f:f + 1], x[:, f:f + 1], gamma.cuda(), beta.cuda(), stats[f:f + 1],
+                         need_dx=False) for f in range(17)]
+    # both sides: at most 128 roundings on terms of |da|(|h| + 1) < 0.2 on
+    # average, over 17 * 65536 pixels
+    tol = 2 * 130 * 2.0 ** -24 * 0.2 * 17 * 65536
+    assert (sum(e[1].double() for e in each) - dg.double()).abs().max() < tol
+    assert (sum(e[2].double() for e in each) - db.double()).abs().max() < tol
+
+
 def test_more_than_2_to_32_bytes():
     """5.4 GB of activations: the last frame's results are those of a call on
     that frame alone, up to the roundings of another chunking."""
