@@ -99,6 +99,7 @@ struct GradBatch {
   int blocks;                // blocks of this batch
   int chunk;                 // elements per block
   int partials;              // of all batches
+  int stream;                // 1: results are stored past the caches
   int inf;                   // the maximum of |g| instead of the 2-norm
   float max_norm;
 };

@@ -20,6 +20,9 @@ namespace {
 bool aligned_to(const void* p, int bytes) { return ((uintptr_t)p % (unsigned)bytes) == 0; }
 bool elt_ok(int t) { return t == CONV3D_ELT_BF16 || t == CONV3D_ELT_FP16 || t == CONV3D_ELT_FP32; }
 
+// Results of more bytes are stored past the caches: half of the memory-side one.
+constexpr long long kStreamBytes = 128LL << 20;
+
 // ------------------------------------------------------------- GroupNorm
 
 constexpr long long kGnMaxItems = (1LL << 24) - 1;   // work-groups of one launch (grid x 256 < 2^32)
@@ -40,7 +43,6 @@ struct GnTrainPlan {
 // 192 and 218 us, left to two passes for that room.)
 constexpr int kGnMaxPieces = 256;
 constexpr int kGnFill = 256;             // work-groups that give every CU one
-constexpr long long kGnStreamBytes = 128LL << 20;    // half of the memory-side cache
 // Rows per thread up to which one work-group per narrow range is better than
 // an exchange, where the chip is not filled ([1,5,32,32,512] bf16 forward, 8
 // rows: 10.0 and 11.2 us; backward, 16 rows: 21.7 and 17.5 us).
@@ -165,7 +167,7 @@ conv3d_status plan_gn_train(const conv3d_group_norm_train_desc* d, bool bwd, GnT
   // the resident form needs its words and channel sums instead
   pl->r = GnResPlan{};
   pl->r.spin = spin_bound();
-  pl->r.stream = prod({units, P, a.C, size}) > kGnStreamBytes;
+  pl->r.stream = prod({units, P, a.C, size}) > kStreamBytes;
   pl->fits = plan_resident(a, bwd, &pl->r);
   if (pl->fits) {
     const GnResPlan& r = pl->r;
@@ -465,12 +467,14 @@ conv3d_status run_grads(const conv3d_grad* g, int count, int norm_type, bool cli
   reads.reserve((size_t)count);
   writes.reserve((size_t)count + 2);
   int last = -1;                         // the last tensor that holds anything
+  long long out_bytes = 0;
   for (int i = 0; i < count; ++i) {
     if (g[i].numel == 0) continue;
     last = i;
     const uintptr_t src = (uintptr_t)g[i].grad;
     if (!src) return CONV3D_ERR_NULL;
     if (src % (unsigned)elt_size(g[i].dtype)) return CONV3D_ERR_ALIGN;
+    out_bytes += g[i].numel * elt_size(g[i].out_dtype);
     const bool in_place = !g[i].out || g[i].out == g[i].grad;
     if (clip && in_place && g[i].out_dtype != g[i].dtype) return CONV3D_ERR_OVERLAP;
     (clip && in_place ? writes : reads)
@@ -494,6 +498,7 @@ conv3d_status run_grads(const conv3d_grad* g, int count, int norm_type, bool cli
   b.norm = norm;
   b.chunk = (int)pl.chunk;
   b.partials = (int)pl.partials;
+  b.stream = out_bytes > kStreamBytes;
   b.inf = norm_type == CONV3D_GRAD_NORM_INF;
   b.max_norm = max_norm;
   for (int pass = 0; pass < (clip ? 2 : 1); ++pass) {

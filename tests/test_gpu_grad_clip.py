@@ -142,6 +142,30 @@ def test_extreme_and_non_finite_values(kind):
     assert torch.all(t == 0)
 
 
+@pytest.mark.parametrize("src,dst", [(torch.bfloat16, torch.float32), (torch.float32, torch.bfloat16),
+                                     (torch.float16, torch.float16), (torch.float32, None)])
+@pytest.mark.parametrize("kind", ["l2", "inf"])
+def test_results_larger_than_the_cache_share(src, dst, kind):
+    """More than 128 MB of results (stored past the caches), at odd addresses."""
+    n = (1 << 26) + 4099
+    g = torch.Generator(device="cuda").manual_seed(4)
+    buf = torch.randn(n + 1, generator=g, device="cuda").to(src)
+    t = buf[1:]
+    before = t.clone()
+    out = None if dst is None else torch.full((n + 3,), 7.0, dtype=dst, device="cuda")
+    limit = 1.0
+    norm = GradClip([t[:5], t[5:]], None if dst is None else [out[1:6], out[6:n + 1]],
+                    norm=kind).clip(limit).double()
+    want = before.double().abs().max() if kind == "inf" else before.double().square().sum().sqrt()
+    assert abs(norm - want) <= 2.0 ** -23 * want
+    got = t if dst is None else out[1:n + 1]
+    ref = before.double() * (limit / (want + 1e-6))
+    tol = (HALF[got.dtype] + 2.0 ** -22) * ref.abs() + (2.0 ** -25 if dst == torch.float16 else 0)
+    assert torch.all((got.double() - ref).abs() <= tol)
+    if dst is not None:
+        assert out[0] == 7.0 and torch.all(out[n + 1:] == 7.0) and torch.equal(t, before)
+
+
 def test_moved_tensors_are_looked_up_again():
     t = draw(5000, torch.float32, 1).cuda()
     op = GradClip([t])
