@@ -809,7 +809,7 @@ int run_fwd(const GnTrainArgs& a, const GnResPlan& r, hipStream_t s) {
   if (r.passes <= 4)
     hipLaunchKernelGGL((gn_resident_fwd_kernel<T, SILU, 4, 0, false, false>), grid, block, 0, s, a,
                        r);
-  else if (r.compact && r.stream)
+  else if (r.compact && a.stream)
     hipLaunchKernelGGL((gn_resident_fwd_kernel<T, SILU, R, L, true, true>), grid, block, 0, s, a,
                        r);
   else if (r.compact)
@@ -838,7 +838,7 @@ int run_bwd(const GnTrainArgs& a, const GnResPlan& r, hipStream_t s) {
   if (r.W > 1 && a.out) clear_words(a, r, s);
   constexpr int R = kGnRowsBwdCompact, L = kGnRowsBwdLds;
   if (r.passes <= 4) start_bwd<T, SILU, 4, 0, false, false>(a, r, s);
-  else if (r.compact && r.stream) start_bwd<T, SILU, R, L, true, true>(a, r, s);
+  else if (r.compact && a.stream) start_bwd<T, SILU, R, L, true, true>(a, r, s);
   else if (r.compact) start_bwd<T, SILU, R, L, true, false>(a, r, s);
   else start_bwd<T, SILU, kGnRows, 0, false, false>(a, r, s);
   if (r.channel_sums)

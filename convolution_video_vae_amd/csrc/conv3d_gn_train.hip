@@ -19,7 +19,10 @@
 //   finalize  chunk pairs in a fixed order -> the group's statistics, or the
 //             unit's channel sums and the group's c1, c2
 //   result    elementwise, from the last chunk back: what the sums pass read
-//             last is still in the memory-side cache
+//             last is still in the memory-side cache. Results that would fill
+//             half of it and more are stored past it ([1,17,256,256,128] bf16
+//             with statistics over the clip, forward 192 -> 162 us, backward
+//             307 -> 287 us)
 //   params    dgamma, dbeta from the units' channel sums, in unit order
 // No atomics: results do not depend on the order of work-groups.
 //
@@ -127,6 +130,15 @@ __device__ __forceinline__ void join_channels(const GnTrainArgs& a, const Rows& 
   }
 }
 
+// A vector of results; STREAM (16-byte vectors): past the caches.
+template <bool STREAM, class T, int VEC>
+__device__ __forceinline__ void store_pack(void* p, const Pack<T, VEC>& v) {
+  if constexpr (STREAM)
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, v), (u32x4_t*)p);
+  else
+    *(Pack<T, VEC>*)p = v;
+}
+
 template <class T, int VEC>
 __global__ __launch_bounds__(kThreads) void gn_train_stats_kernel(GnTrainArgs a, Rows r) {
   typedef typename T::store E;
@@ -209,7 +221,7 @@ __global__ __launch_bounds__(kThreads) void gn_train_stats_finalize_kernel(GnTra
   }
 }
 
-template <class T, int VEC, bool SILU>
+template <class T, int VEC, bool SILU, bool STREAM>
 __global__ __launch_bounds__(kThreads) void gn_train_apply_kernel(GnTrainArgs a, Rows r) {
   typedef typename T::store E;
   constexpr int U = 8;
@@ -241,7 +253,7 @@ __global__ __launch_bounds__(kThreads) void gn_train_apply_kernel(GnTrainArgs a,
           f[j] = fmaf(f[j] - mean[j], scale[j], beta[j]);
           if (SILU) f[j] = silu_of<T::kWide>(f[j]);
         }
-        *(Pack<T, VEC>*)(y + q * yp) = pack<T, VEC>(f);
+        store_pack<STREAM>(y + q * yp, pack<T, VEC>(f));
       });
 }
 
@@ -344,7 +356,7 @@ __global__ __launch_bounds__(kThreads) void gn_train_bwd_finalize_kernel(GnTrain
   }
 }
 
-template <class T, int VEC, bool SILU>
+template <class T, int VEC, bool SILU, bool STREAM>
 __global__ __launch_bounds__(kThreads) void gn_train_bwd_apply_kernel(GnTrainArgs a, Rows r) {
   typedef typename T::store E;
   constexpr int U = 4;
@@ -382,7 +394,7 @@ __global__ __launch_bounds__(kThreads) void gn_train_bwd_apply_kernel(GnTrainArg
           b.value(j, f[j], d[j], h, da);
           f[j] = gn_dx(b.rstd[j], b.gamma[j], da, c1[j], h, c2[j]);
         }
-        *(Pack<T, VEC>*)(dx + q * op) = pack<T, VEC>(f);
+        store_pack<STREAM>(dx + q * op, pack<T, VEC>(f));
       });
 }
 
@@ -442,16 +454,29 @@ bool rows_for(const GnTrainArgs& a, int vec, bool bwd, Rows* r) {
   return true;
 }
 
+// Only 16-byte vectors are stored past the caches.
+template <class T, int VEC>
+constexpr bool kStreams = VEC * sizeof(typename T::store) == 16;
+
+template <class T, int VEC, bool SILU>
+void start_apply(const GnTrainArgs& a, const Rows& r, dim3 grid, bool stream, hipStream_t s) {
+  if (stream)
+    hipLaunchKernelGGL((gn_train_apply_kernel<T, VEC, SILU, kStreams<T, VEC>>), grid,
+                       dim3(kThreads), 0, s, a, r);
+  else
+    hipLaunchKernelGGL((gn_train_apply_kernel<T, VEC, SILU, false>), grid, dim3(kThreads), 0, s, a,
+                       r);
+}
+
 template <class T, int VEC>
 int run_fwd(const GnTrainArgs& a, const Rows& r, hipStream_t s) {
   const dim3 grid((unsigned)a.units * (unsigned)a.chunks, r.tiles);
   hipLaunchKernelGGL((gn_train_stats_kernel<T, VEC>), grid, dim3(kThreads), 0, s, a, r);
   hipLaunchKernelGGL(gn_train_stats_finalize_kernel, dim3((unsigned)a.units * (unsigned)a.G),
                      dim3(kThreads), 0, s, a);
-  if (a.silu)
-    hipLaunchKernelGGL((gn_train_apply_kernel<T, VEC, true>), grid, dim3(kThreads), 0, s, a, r);
-  else
-    hipLaunchKernelGGL((gn_train_apply_kernel<T, VEC, false>), grid, dim3(kThreads), 0, s, a, r);
+  const bool stream = a.stream && kStreams<T, VEC>;
+  if (a.silu) start_apply<T, VEC, true>(a, r, grid, stream, s);
+  else start_apply<T, VEC, false>(a, r, grid, stream, s);
   return (int)hipGetLastError();
 }
 
@@ -461,9 +486,12 @@ int run_bwd_act(const GnTrainArgs& a, const Rows& r, hipStream_t s) {
   hipLaunchKernelGGL((gn_train_bwd_sums_kernel<T, VEC, SILU>), grid, dim3(kThreads), 0, s, a, r);
   hipLaunchKernelGGL(gn_train_bwd_finalize_kernel, dim3((unsigned)a.units * (unsigned)a.G),
                      dim3(kThreads), 0, s, a);
-  if (a.out)
-    hipLaunchKernelGGL((gn_train_bwd_apply_kernel<T, VEC, SILU>), grid, dim3(kThreads), 0, s, a,
-                       r);
+  if (a.out && a.stream && kStreams<T, VEC>)
+    hipLaunchKernelGGL((gn_train_bwd_apply_kernel<T, VEC, SILU, kStreams<T, VEC>>), grid,
+                       dim3(kThreads), 0, s, a, r);
+  else if (a.out)
+    hipLaunchKernelGGL((gn_train_bwd_apply_kernel<T, VEC, SILU, false>), grid, dim3(kThreads), 0,
+                       s, a, r);
   if (a.dgamma || a.dbeta)
     hipLaunchKernelGGL(gn_train_params_kernel, dim3((a.C + 31) / 32), dim3(kThreads), 0, s, a);
   return (int)hipGetLastError();

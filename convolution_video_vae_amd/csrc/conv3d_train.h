@@ -34,6 +34,7 @@ struct GnTrainArgs {
   int C, G, cpg;
   int units, chunks, chunk_px;              // chunk_px is a multiple of 8
   int dtype, silu;
+  int stream;                // 1: results are stored past the caches
   float eps;
 };
 int launch_gn_train_fwd(const GnTrainArgs& args, void* stream);
@@ -53,7 +54,6 @@ constexpr int kGnCompact = 128;                        // values of a row in the
 struct GnResPlan {
   int Cb, Vb, NR, Gb;
   int ppi, passes, piece_px, W;
-  int stream;                // 1: results are stored past the caches (compact form)
   int lanes;                 // 1: a row is a power of two of lanes (at most a wave)
   int compact;               // 1: lanes, and at most kGnCompact channels (backward) or slots
   int fold;                  // channels of a vector that always share a group (a power of two)

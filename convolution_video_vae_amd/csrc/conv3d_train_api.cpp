@@ -155,6 +155,7 @@ conv3d_status plan_gn_train(const conv3d_group_norm_train_desc* d, bool bwd, GnT
   a.chunk_px = (int)chunk;
   a.dtype = d->dtype;
   a.silu = d->silu ? 1 : 0;
+  a.stream = prod({units, P, a.C, size}) > kStreamBytes;
   a.eps = d->eps;
   size_t at = (size_t)units * chunks * a.C * 16;
   pl->off_chan = at = (at + 255) / 256 * 256;
@@ -167,7 +168,6 @@ conv3d_status plan_gn_train(const conv3d_group_norm_train_desc* d, bool bwd, GnT
   // the resident form needs its words and channel sums instead
   pl->r = GnResPlan{};
   pl->r.spin = spin_bound();
-  pl->r.stream = prod({units, P, a.C, size}) > kStreamBytes;
   pl->fits = plan_resident(a, bwd, &pl->r);
   if (pl->fits) {
     const GnResPlan& r = pl->r;
