@@ -47,7 +47,7 @@ constexpr int kGnFill = 256;             // work-groups that give every CU one
 // an exchange, where the chip is not filled ([1,5,32,32,512] bf16 forward, 8
 // rows: 10.0 and 11.2 us; backward, 16 rows: 21.7 and 17.5 us).
 constexpr int kGnAloneRows = 10;
-constexpr int kGnSpin = 20000;           // polls (some 20 ms) before a work-group helps itself
+constexpr int kGnSpin = 5000;            // polls (some 5 ms) before a work-group helps itself
 
 // CONV3D_GN_SPIN: another bound, for tests (0: no work-group waits, each forms
 // the sums of its unit's other pieces itself).

@@ -321,17 +321,18 @@ def replay_check(run, inputs, refill):
             assert torch.equal(o, w), f"replay {i}"
 
 
-def test_graph_replays():
-    shape = (1, 3, 24, 20, 128)
+@pytest.mark.parametrize("shape", [(1, 3, 24, 20, 128), (1, 2, 64, 65, 128), (1, 2, 61, 67, 45)])
+def test_graph_replays(shape):
+    c = shape[4]
     x, dy = (torch.zeros(shape, dtype=torch.bfloat16, device="cuda") for _ in range(2))
-    gamma, beta = (p.cuda() for p in params(128, 24))
-    op = GroupNormTrain(shape, 32, silu=True)
-    ns = NormSiluBackward(shape, bias=True)
+    gamma, beta = (p.cuda() for p in params(c, 24))
+    op = GroupNormTrain(shape, 32 if c == 128 else 15, silu=True)
+    ns = NormSiluBackward(shape, bias=True) if c % 8 == 0 else None
 
     def run():
         y, stats = op.forward(x, gamma, beta)
-        return [y, stats, *op.backward(dy, x, gamma, beta, stats),
-                *ns(x, dy, gamma.bfloat16())]
+        outs = [y, stats, *op.backward(dy, x, gamma, beta, stats)]
+        return outs + (list(ns(x, dy, gamma.bfloat16())) if ns else [])
 
     def refill(i):
         x.copy_(draw(shape, torch.bfloat16, 30 + i))
@@ -339,6 +340,38 @@ def test_graph_replays():
 
     refill(9)
     replay_check(run, (x, dy), refill)
+
+
+def test_two_graphs_side_by_side():
+    """Two graphs captured from one object, replayed on two streams at once:
+    each has its scratch memory in its own pool."""
+    shape = (1, 4, 96, 96, 128)
+    op = GroupNormTrain(shape, 32, silu=True)
+    gamma, beta = (p.cuda() for p in params(128, 27))
+    xs = [draw(shape, torch.bfloat16, 60 + i).cuda() for i in range(2)]
+    want = []
+    for x in xs:
+        y, st = op.forward(x, gamma, beta)
+        want.append((y, st, *op.backward(x, x, gamma, beta, st)))
+    graphs, outs = [], []
+    for x in xs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y, st = op.forward(x, gamma, beta)
+            outs.append((y, st, *op.backward(x, x, gamma, beta, st)))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(3):
+        for o in outs:
+            for t in o:
+                t.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(o, w))
 
 
 def test_two_streams_at_once():
