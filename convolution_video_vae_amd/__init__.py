@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -523,10 +524,10 @@ def conv3d_norm_silu_bwd(value, dy, dskip, n: int, d: int, h: int, w: int, c: in
 def make_grads(grads: Sequence[tuple]):
     """Gradient list of the calls below from (grad, out, numel, dtype,
     out_dtype) tuples (addresses, ELT_* types; out None: in place)."""
-    arr = (conv3d_grad * len(grads))()
-    for e, (g, o, numel, dtype, out_dtype) in zip(arr, grads):
-        e.grad, e.out, e.numel, e.dtype, e.out_dtype = _ptr(g), _ptr(o), numel, dtype, out_dtype
-    return arr
+    flat = []
+    for g, o, numel, dtype, out_dtype in grads:
+        flat += (_ptr(g) or 0, _ptr(o) or 0, numel, dtype, out_dtype)
+    return (conv3d_grad * len(grads)).from_buffer_copy(struct.pack("QQqii" * len(grads), *flat))
 
 
 def conv3d_grad_workspace_bytes(grads) -> int:

@@ -415,8 +415,10 @@ def _dense(t: torch.Tensor) -> bool:
 class GradClip:
     """Global norm of many gradient tensors (bf16, fp16 or fp32, mixed), and
     clipping, in place or into `outs` (same shapes and strides, any of the
-    types). The lists are kept; a tensor whose memory has moved since the
-    last call is looked up again."""
+    types). The lists are kept, and so is the memory that the tensors had at
+    the last call: a tensor that has moved since (`t.data = ...`) is looked up
+    again, and none moves to where another was. A tensor that stays where it
+    is keeps its size and strides."""
 
     def __init__(self, grads: Sequence[torch.Tensor],
                  outs: Optional[Sequence[torch.Tensor]] = None, *, norm: str = "l2"):
@@ -434,19 +436,26 @@ class GradClip:
         self._build()
 
     def _build(self) -> None:
-        for i, t in enumerate(self._all):
-            if not t.is_cuda or t.device != self.device or t.dtype not in _ELT or not _dense(t):
+        index = self.device.index if self.device.type == "cuda" else None
+        kinds = [_ELT.get(t.dtype) for t in self._all]
+        dense = list(map(torch.Tensor.is_contiguous, self._all))
+        for i, (t, kind, dev) in enumerate(zip(self._all, kinds,
+                                               map(torch.Tensor.get_device, self._all))):
+            if kind is None or dev != index or not (dense[i] or _dense(t)):
                 raise ValueError(f"gradient {i % len(self.grads)} must be a dense bf16, fp16 or "
                                  f"fp32 tensor on {self.device}, got {tuple(t.shape)} {t.dtype} "
                                  f"strides {tuple(t.stride())} on {t.device}")
-        for i, (g, o) in enumerate(zip(self.grads, self.outs or [])):
-            if g.shape != o.shape or (g.stride() != o.stride()
-                                      and not (g.is_contiguous() and o.is_contiguous())):
+        n = len(self.grads)
+        for i, o in enumerate(self.outs or []):
+            g = self.grads[i]
+            if g.shape != o.shape or (g.stride() != o.stride() and not (dense[i] and dense[n + i])):
                 raise ValueError(f"out {i} differs from its gradient in shape or strides")
-        self._ptrs = [t.data_ptr() for t in self._all]
-        self._table = make_grads([(g, o, g.numel(), _ELT[g.dtype], _ELT[(o if o is not None
-                                                                          else g).dtype])
-                                  for g, o in zip(self.grads, self.outs or [None] * len(self.grads))])
+        # held, so that an address that has not changed is still the same memory
+        self._held = list(map(torch.Tensor.untyped_storage, self._all))
+        self._ptrs = list(map(torch.Tensor.data_ptr, self._all))
+        self._table = make_grads(list(zip(self._ptrs, self._ptrs[n:] or [None] * n,
+                                          map(torch.Tensor.numel, self.grads), kinds,
+                                          kinds[n:] or kinds)))
         self._ws = conv3d_grad_workspace_bytes(self._table)
 
     def _call(self, run):

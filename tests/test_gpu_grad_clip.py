@@ -177,6 +177,19 @@ def test_moved_tensors_are_looked_up_again():
     assert keep is not None
 
 
+def test_moved_to_a_smaller_size():
+    """The old memory is not handed out again while its address stands for the
+    old size."""
+    t = torch.full((4096,), 2.0, device="cuda")
+    op = GradClip([t])
+    assert op.norm().item() == 128.0  # sqrt(4096 * 4)
+    before = t.data_ptr()
+    t.data = torch.empty(0, device="cuda")
+    t.data = torch.ones(1024, device="cuda")
+    assert t.data_ptr() != before
+    assert op.norm().item() == 32.0
+
+
 def test_more_than_2_to_32_elements():
     n = (1 << 32) + 4099
     t = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
