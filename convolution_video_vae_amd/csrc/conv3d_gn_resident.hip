@@ -39,6 +39,8 @@
 namespace conv3d {
 namespace {
 
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+
 constexpr unsigned long long kEmpty = ~0ull;
 
 // Two sums as one word that is never kEmpty: NaNs get one pattern.
@@ -121,7 +123,28 @@ struct GroupOf {
 //
 // Where a row's vectors are a power of two of lanes, rows of one wave are
 // joined by exchanges between lanes and only one value per wave goes through
-// LDS; else every lane's goes. Either way in a fixed order.
+// LDS; else every lane's goes. Either way in a fixed order. Rows of at most 16
+// lanes leave a quarter of the values to each quarter of the wave: 16 values of
+// 8 lanes take 16 exchanges instead of 48. (With da and h kept where R <= 4 and
+// both sums of a group in one pass: H3 L0 backward 205 -> 194.5 us,
+// [1,5,16,16,1024] bf16 backward 12.1 -> 9.3 us.)
+
+// Lanes below 32: the sum of a of lane and lane + 32; the others: of b of lane
+// and lane - 32. (The elements are copied first: a bit cast of one in place
+// reads element 0.)
+__device__ __forceinline__ float halves(float a, float b) {
+  const auto v = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, a),
+                                                  __builtin_bit_cast(unsigned, b), false, false);
+  const unsigned lo = v[0], hi = v[1];
+  return __builtin_bit_cast(float, lo) + __builtin_bit_cast(float, hi);
+}
+// The same between the two rows of 16 lanes of each half.
+__device__ __forceinline__ float rows16(float a, float b) {
+  const auto v = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, a),
+                                                  __builtin_bit_cast(unsigned, b), false, false);
+  const unsigned lo = v[0], hi = v[1];
+  return __builtin_bit_cast(float, lo) + __builtin_bit_cast(float, hi);
+}
 
 // Channel sums of N quantities: s[k][j] of every thread -> tot[k][channel].
 // COMPACT (the lanes' form, at most kGnCompact values of a row): small arrays,
@@ -133,7 +156,18 @@ struct ChannelSums {
   __device__ __forceinline__ void join(const GnResPlan& r, bool active, float (&s)[N][VEC]) {
     const int t = threadIdx.x;
     const bool lanes = COMPACT || r.lanes;
-    if (lanes) {
+    const bool quarters = N == 2 && lanes && r.Vb <= 16;
+    if (quarters) {
+      // two quantities' halves of the wave change places and are added: a
+      // quarter of the wave is left with a quarter of the values
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) s[0][j] = halves(s[0][j], s[N - 1][j]);
+#pragma unroll
+      for (int j = 0; j < VEC / 2; ++j) s[0][j] = rows16(s[0][j], s[0][j + VEC / 2]);
+      for (int m = r.Vb; m < 16; m <<= 1)
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) s[0][j] += __shfl_xor(s[0][j], m);
+    } else if (lanes) {
       for (int m = r.Vb; m < 64; m <<= 1)
 #pragma unroll
         for (int k = 0; k < N; ++k)
@@ -141,8 +175,13 @@ struct ChannelSums {
           for (int j = 0; j < VEC; ++j) s[k][j] += __shfl_xor(s[k][j], m);
     }
     const int rows = lanes ? NT / 64 : r.ppi;
-    const int at = lanes ? (t >> 6) * r.Cb + (t & 63) * VEC : t * VEC;
-    if (lanes ? (t & 63) < r.Vb : active) {
+    const int at = lanes ? (t >> 6) * r.Cb + (t & (quarters ? 15 : 63)) * VEC : t * VEC;
+    if (quarters) {
+      if ((t & 15) < r.Vb)
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j)
+          red[(t >> 5) & 1][at + (t & 16 ? VEC / 2 : 0) + j] = s[0][j];
+    } else if (lanes ? (t & 63) < r.Vb : active) {
 #pragma unroll
       for (int k = 0; k < N; ++k)
 #pragma unroll
@@ -263,23 +302,34 @@ struct GroupMoments {
   }
 };
 
-// f(g, sum over group g of v(channel)) for every group of the range: by one
-// thread for few channels, by a wave for many.
+// use(g, the sums over group g of the two values of v(channel)) for every group
+// of the range: by one thread for few channels, by a wave for many.
 template <int NT, class Value, class Use>
 __device__ __forceinline__ void each_group(int Gb, int cpg, Value value, Use use) {
   if (cpg <= 16) {
     for (int g = threadIdx.x; g < Gb; g += NT) {
-      float v = value(g * cpg);
-      for (int c = 1; c < cpg; ++c) v += value(g * cpg + c);
+      f32x2_t v = value(g * cpg);
+      for (int c = 1; c < cpg; ++c) {
+        const f32x2_t o = value(g * cpg + c);
+        v[0] += o[0];
+        v[1] += o[1];
+      }
       use(g, v);
     }
   } else {
     const int lane = threadIdx.x & 63;
     for (int g = threadIdx.x >> 6; g < Gb; g += NT / 64) {
-      float v = 0.0f;
-      for (int c = lane; c < cpg; c += 64) v += value(g * cpg + c);
+      f32x2_t v = {0.0f, 0.0f};
+      for (int c = lane; c < cpg; c += 64) {
+        const f32x2_t o = value(g * cpg + c);
+        v[0] += o[0];
+        v[1] += o[1];
+      }
 #pragma unroll
-      for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
+      for (int m = 32; m > 0; m >>= 1) {
+        v[0] += __shfl_xor(v[0], m);
+        v[1] += __shfl_xor(v[1], m);
+      }
       if (lane == 0) use(g, v);
     }
   }
@@ -602,8 +652,8 @@ struct BwdValues {
   }
 };
 
-// R <= 4 rows: few values, where the terms of dx may cancel: gn_dx, and da
-// formed again. More rows: da is kept in the place of dy, of LROWS rows in LDS,
+// R <= 4 rows: few values, where the terms of dx may cancel: gn_dx, of da and h
+// as they were. More rows: da is kept in the place of dy, of LROWS rows in LDS,
 // and dx is two products per value. GV groups at most share a vector's channels: VEC, or
 // a quarter of that where every four channels are of one group.
 template <class T, bool SILU, int R, int LROWS, int GV, bool COMPACT, bool STREAM>
@@ -623,7 +673,7 @@ __global__ __launch_bounds__(kGnResThreadsBwd, 2) void gn_resident_bwd_kernel(Gn
   long long first;
   const int n = rows_of(a, r, h, h.w, &first);
   Held<T> vx[R], vd[R];
-  float vda[FEW ? 1 : R - LROWS][VEC];
+  float vda[R - LROWS][VEC], vh[FEW ? R : 1][VEC];
   BwdValues<T, SILU, VEC, GV> bv;
   // ahead of the rows, as in the forward pass
   if (threadIdx.x < r.Cb) lgamma[threadIdx.x] = a.gamma[h.range * r.Cb + threadIdx.x];
@@ -652,12 +702,12 @@ __global__ __launch_bounds__(kGnResThreadsBwd, 2) void gn_resident_bwd_kernel(Gn
   // (sum of gamma da, of gamma da h) of a piece's groups, as words
   const auto piece = [&](float (&s)[2][VEC]) {
     sums.join(r, h.active, s);
-    each_group<NT>(r.Gb, a.cpg, [&](int c) { return mul_alone(lgamma[c], sums.tot[1][c]); },
-                   [&](int g, float t) { g1[g] = t; });
-    each_group<NT>(r.Gb, a.cpg, [&](int c) { return mul_alone(lgamma[c], sums.tot[0][c]); },
-                   [&](int g, float t) { g2[g] = t; });
-    __syncthreads();
-    for (int g = threadIdx.x; g < r.Gb; g += NT) pieces.own[g] = word_of(g1[g], g2[g]);
+    each_group<NT>(
+        r.Gb, a.cpg,
+        [&](int c) {
+          return f32x2_t{mul_alone(lgamma[c], sums.tot[1][c]), mul_alone(lgamma[c], sums.tot[0][c])};
+        },
+        [&](int g, const f32x2_t& v) { pieces.own[g] = word_of(v[0], v[1]); });
     __syncthreads();
   };
   const auto add = [&](float (&s)[2][VEC], int j, float hh, float da) {
@@ -677,7 +727,8 @@ __global__ __launch_bounds__(kGnResThreadsBwd, 2) void gn_resident_bwd_kernel(Gn
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         add(s, j, f[j], d[j]);
-        if (!FEW && i >= LROWS) vda[FEW ? 0 : i - LROWS][j] = d[j];
+        if (i >= LROWS) vda[i - LROWS][j] = d[j];
+        if (FEW) vh[FEW ? i : 0][j] = f[j];
       }
       if (i < LROWS) {
 #pragma unroll
@@ -764,10 +815,7 @@ __global__ __launch_bounds__(kGnResThreadsBwd, 2) void gn_resident_bwd_kernel(Gn
     if (i < n) {
       float f[VEC], d[VEC];
       vx[i].get(f);
-      if (FEW) {
-        vd[i].get(d);
-        bv.run(f, d);
-      } else if (i < LROWS) {
+      if (i < LROWS) {
 #pragma unroll
         for (int j = 0; j < VEC; j += 4) {
           const f32x4_t q = lds_da[i][j / 4][threadIdx.x];
@@ -783,7 +831,7 @@ __global__ __launch_bounds__(kGnResThreadsBwd, 2) void gn_resident_bwd_kernel(Gn
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         if (FEW)
-          f[j] = gn_dx(bv.rstd[bv.at(j)], gam[j], d[j], c1[j], f[j], c2[j]);
+          f[j] = gn_dx(bv.rstd[bv.at(j)], gam[j], d[j], c1[j], vh[FEW ? i : 0][j], c2[j]);
         else
           f[j] = fmaf(d[j], gam[j],
                       fmaf(T::kWide ? bv.h(j, f[j]) : f[j], c2[j], c1[j]));
