@@ -12,8 +12,10 @@
 // Rows are loaded as non-temporal: they are read once, and what they would
 // push out of the memory-side cache are dirty lines of y or dx, whose
 // write-back then competes with the loads (H3 L0 forward 134 -> 128 us,
-// backward 218 -> 209 us). So are results stored that would fill half of that
-// cache and more (121 and 205 us); smaller ones stay there for their reader.
+// backward 218 -> 209 us when this came in). So are results stored that would
+// fill half of that cache and more (128 -> 121 and 209 -> 205 us); smaller ones
+// stay there for their reader. H3 L0 now: 121 and 193 us, 91 and 86 % of a
+// copy's rate.
 //
 // The exchange. Each piece publishes one 64-bit word per group (two fp32
 // sums) with a relaxed agent-scope atomic store, and reads the others' words
