@@ -422,6 +422,9 @@ BIG_SHAPES = [
     ((2, 3, 32, 40, 64), 8, True, False), ((1, 1, 100, 90, 96), 32, True, True),
     ((1, 1, 64, 64, 480), 30, True, True), ((1, 1, 700, 720, 16), 4, True, True),
     ((1, 1, 50, 60, 1024), 4, True, True),
+    # groups of 64 and 128 channels
+    ((1, 2, 30, 31, 256), 2, True, True), ((1, 1, 50, 60, 512), 4, False, True),
+    ((1, 1, 30, 40, 192), 3, True, False), ((2, 1, 3, 5, 256), 4, True, True),
 ]
 
 
