@@ -232,7 +232,8 @@ def make_epilogue(bias=None, residual=None, gamma=None, residual_out=None,
     return e
 
 
-_DTYPE_NAMES = {"bf16": "bfloat16", "fp32": "float32"}
+_DTYPE_NAMES = {"bf16": "bfloat16", "fp16": "float16", "fp32": "float32"}
+_ELT_NAMES = {ELT_BF16: "bf16", ELT_FP16: "fp16", ELT_FP32: "fp32"}
 
 
 def _check_buffer(t, nbytes: int, what: str, dtype: Optional[str] = None) -> None:
@@ -269,6 +270,35 @@ def _check_conv_buffers(desc: conv3d_desc, x, w_packed, epi: Optional[conv3d_epi
         _check_buffer(t.get("gamma"), 2 * desc.cout, "gamma", "bf16")
         _check_buffer(t.get("residual"), out_bytes, "residual", "bf16")
         _check_buffer(t.get("residual_out"), out_bytes, "residual_out", "bf16")
+
+
+def _check_span(t, nbytes: int, what: str, elt: int) -> None:
+    """The same for a tensor whose rows may lie apart (a channel slice of a
+    wider one): its storage must reach nbytes from its first element."""
+    if t is None or isinstance(t, int):
+        return
+    if not getattr(t, "is_cuda", False):
+        raise ValueError(f"{what} must be a GPU tensor")
+    if str(t.dtype) != "torch." + _DTYPE_NAMES[_ELT_NAMES[elt]]:
+        raise ValueError(f"{what} must be {_ELT_NAMES[elt]}, got {t.dtype}")
+    have = t.untyped_storage().nbytes() - t.storage_offset() * t.element_size()
+    if have < nbytes:
+        raise ValueError(f"{what} holds {have} bytes, the call needs {nbytes}")
+
+
+def _check_group_norm_train(desc: conv3d_group_norm_train_desc, workspace, workspace_bytes: int,
+                            stats, activations, vectors) -> None:
+    """activations: (tensor, pitch, name); vectors: (tensor, name) of c fp32 values."""
+    if desc.dtype in _ELT_NAMES:                       # else the library refuses the call
+        size = 4 if desc.dtype == ELT_FP32 else 2
+        for t, pitch, what in activations:
+            rows = desc.n * desc.d * desc.h * desc.w - 1
+            _check_span(t, (rows * (pitch or desc.c) + desc.c) * size, what, desc.dtype)
+    for t, what in vectors:
+        _check_buffer(t, 4 * desc.c, what, "fp32")
+    units = desc.n * (desc.d if desc.t_isolated else 1)
+    _check_buffer(stats, 8 * units * desc.groups, "stats", "fp32")
+    _check_workspace(workspace, workspace_bytes)
 
 
 def _check_workspace(workspace, workspace_bytes: int) -> None:
@@ -466,9 +496,10 @@ def conv3d_norm_silu(x, n: int, d: int, h: int, w: int, c: int, epi: conv3d_epil
 
 
 # --------------------------------------------------------------------------- training
-# These take the buffers as the C entry points do (raw addresses or tensors,
-# sized by the caller); layer.GroupNormTrain, layer.NormSiluBackward and
-# layer.GradClip check tensors and allocate.
+# These take the buffers as the C entry points do: tensors, whose types and
+# sizes are checked, or raw addresses (where x, value or a gradient is one,
+# those beside it are the caller's responsibility too). layer.GroupNormTrain,
+# layer.NormSiluBackward and layer.GradClip check tensors by shape and allocate.
 
 def make_group_norm_train_desc(x_shape: Sequence[int], groups: int, *, eps: float = 1e-5,
                                silu: bool = False, t_isolated: bool = True, dtype: int = ELT_BF16,
@@ -491,6 +522,10 @@ def conv3d_group_norm_train_workspace_bytes(desc: conv3d_group_norm_train_desc,
 
 def conv3d_group_norm_train_fwd(desc: conv3d_group_norm_train_desc, x, gamma, beta, y, stats,
                                 workspace, workspace_bytes: int, stream=None) -> None:
+    if not isinstance(x, int):
+        _check_group_norm_train(desc, workspace, workspace_bytes, stats,
+                                ((x, desc.x_pitch, "x"), (y, desc.y_pitch, "y")),
+                                ((gamma, "gamma"), (beta, "beta")))
     _check(lib().conv3d_group_norm_train_fwd(ctypes.byref(desc), _ptr(x), _ptr(gamma), _ptr(beta),
                                              _ptr(y), _ptr(stats), _ptr(workspace),
                                              workspace_bytes, _stream(stream)),
@@ -500,6 +535,12 @@ def conv3d_group_norm_train_fwd(desc: conv3d_group_norm_train_desc, x, gamma, be
 def conv3d_group_norm_train_bwd(desc: conv3d_group_norm_train_desc, dy, x, gamma, beta, stats, dx,
                                 dgamma, dbeta, workspace, workspace_bytes: int,
                                 stream=None) -> None:
+    if not isinstance(x, int):
+        _check_group_norm_train(desc, workspace, workspace_bytes, stats,
+                                ((dy, desc.y_pitch, "dy"), (x, desc.x_pitch, "x"),
+                                 (dx, desc.dx_pitch, "dx")),
+                                ((gamma, "gamma"), (beta, "beta"), (dgamma, "dgamma"),
+                                 (dbeta, "dbeta")))
     _check(lib().conv3d_group_norm_train_bwd(ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(gamma),
                                              _ptr(beta), _ptr(stats), _ptr(dx), _ptr(dgamma),
                                              _ptr(dbeta), _ptr(workspace), workspace_bytes,
@@ -515,6 +556,13 @@ def conv3d_norm_silu_bwd_workspace_bytes(n: int, d: int, h: int, w: int, c: int)
 
 def conv3d_norm_silu_bwd(value, dy, dskip, n: int, d: int, h: int, w: int, c: int, gamma, dvalue,
                          dgamma, dbias, workspace, workspace_bytes: int, stream=None) -> None:
+    if not isinstance(value, int):
+        for t, what in ((value, "value"), (dy, "dy"), (dskip, "dskip"), (dvalue, "dvalue")):
+            _check_buffer(t, n * d * h * w * c * 2, what, "bf16")
+        _check_buffer(gamma, 2 * c, "gamma", "bf16")
+        _check_buffer(dgamma, 4 * c, "dgamma", "fp32")
+        _check_buffer(dbias, 4 * c, "dbias", "fp32")
+        _check_workspace(workspace, workspace_bytes)
     _check(lib().conv3d_norm_silu_bwd(_ptr(value), _ptr(dy), _ptr(dskip), n, d, h, w, c,
                                       _ptr(gamma), _ptr(dvalue), _ptr(dgamma), _ptr(dbias),
                                       _ptr(workspace), workspace_bytes, _stream(stream)),
@@ -526,6 +574,10 @@ def make_grads(grads: Sequence[tuple]):
     out_dtype) tuples (addresses, ELT_* types; out None: in place)."""
     flat = []
     for g, o, numel, dtype, out_dtype in grads:
+        if not isinstance(g, int):
+            for t, elt in ((g, dtype), (o, out_dtype)):
+                if elt in _ELT_NAMES:
+                    _check_span(t, numel * (4 if elt == ELT_FP32 else 2), "a gradient", elt)
         flat += (_ptr(g) or 0, _ptr(o) or 0, numel, dtype, out_dtype)
     return (conv3d_grad * len(grads)).from_buffer_copy(struct.pack("QQqii" * len(grads), *flat))
 
@@ -539,12 +591,16 @@ def conv3d_grad_workspace_bytes(grads) -> int:
 
 def conv3d_grad_norm(grads, norm_type: int, norm, workspace, workspace_bytes: int,
                      stream=None) -> None:
+    _check_buffer(norm, 4, "norm", "fp32")
+    _check_workspace(workspace, workspace_bytes)
     _check(lib().conv3d_grad_norm(grads, len(grads), norm_type, _ptr(norm), _ptr(workspace),
                                   workspace_bytes, _stream(stream)), "conv3d_grad_norm")
 
 
 def conv3d_grad_clip(grads, norm_type: int, max_norm: float, norm, workspace,
                      workspace_bytes: int, stream=None) -> None:
+    _check_buffer(norm, 4, "norm", "fp32")
+    _check_workspace(workspace, workspace_bytes)
     _check(lib().conv3d_grad_clip(grads, len(grads), norm_type, max_norm, _ptr(norm),
                                   _ptr(workspace), workspace_bytes, _stream(stream)),
            "conv3d_grad_clip")

@@ -322,7 +322,7 @@ class GroupNormTrain:
         else:
             _vector(stats, self._stats_numel, torch.float32, dev, "stats")
         ws = torch.empty(self._ws[0], dtype=torch.uint8, device=dev)
-        conv3d_group_norm_train_fwd(self._desc(xp, yp, yp), x, gamma, beta, y, stats, ws,
+        conv3d_group_norm_train_fwd(self._desc(xp, yp, yp), x.data_ptr(), gamma, beta, y, stats, ws,
                                     self._ws[0], _current_stream(dev.index))
         return y, stats
 
@@ -354,8 +354,8 @@ class GroupNormTrain:
             dgamma = torch.empty(self.c, dtype=torch.float32, device=dev)
             dbeta = torch.empty(self.c, dtype=torch.float32, device=dev)
         ws = torch.empty(self._ws[1], dtype=torch.uint8, device=dev)
-        conv3d_group_norm_train_bwd(self._desc(xp, dp, op), dy, x, gamma, beta, stats, dx, dgamma,
-                                    dbeta, ws, self._ws[1], _current_stream(dev.index))
+        conv3d_group_norm_train_bwd(self._desc(xp, dp, op), dy, x.data_ptr(), gamma, beta, stats, dx,
+                                    dgamma, dbeta, ws, self._ws[1], _current_stream(dev.index))
         return dx, dgamma, dbeta
 
 
@@ -395,8 +395,8 @@ class NormSiluBackward:
         ws = None
         if self.want_gamma or self.want_bias:
             ws = torch.empty(self._ws, dtype=torch.uint8, device=dev)
-        conv3d_norm_silu_bwd(value, dy, dskip, n, d, h, w, c, gamma, dvalue, dgamma, dbias, ws,
-                             self._ws, _current_stream(dev.index))
+        conv3d_norm_silu_bwd(value.data_ptr(), dy, dskip, n, d, h, w, c, gamma, dvalue, dgamma, dbias,
+                             ws, self._ws, _current_stream(dev.index))
         return dvalue, dgamma, dbias
 
 
@@ -465,8 +465,8 @@ class GradClip:
         if list(map(torch.Tensor.data_ptr, self._all)) != self._ptrs:
             self._build()
         norm = torch.empty((), dtype=torch.float32, device=self.device)
-        run(norm, torch.empty(self._ws, dtype=torch.uint8, device=self.device),
-            _current_stream(self.device.index))
+        ws = torch.empty(self._ws, dtype=torch.uint8, device=self.device)
+        run(norm.data_ptr(), ws.data_ptr(), _current_stream(self.device.index))
         return norm
 
     def norm(self) -> torch.Tensor:

@@ -211,3 +211,61 @@ def test_dense_tensors():
     assert layer._dense(t) and layer._dense(t.permute(2, 0, 1)) and layer._dense(t[1])
     assert not layer._dense(t[:, :3]) and not layer._dense(t[0].expand(4, 6, 8))
     assert layer._dense(torch.zeros(())) and layer._dense(torch.zeros(0))
+
+
+class FakeTensor:
+    """What the binding asks of a GPU tensor, on the host."""
+
+    is_cuda = True
+
+    def __init__(self, t):
+        self.t = t
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_bindings_check_tensors():
+    """Short buffers and other types are refused before the library is called
+    (addresses of host memory would be accepted by it)."""
+    def z(*shape, dtype=torch.float32):
+        return FakeTensor(torch.zeros(*shape, dtype=dtype))
+
+    d = cv.make_group_norm_train_desc((1, 2, 3, 4, 16), 4, dtype=cv.ELT_BF16, x_pitch=32)
+    b16 = torch.bfloat16
+    x, y, v, stats = z(24 * 32 - 16, dtype=b16), z(24, 16, dtype=b16), z(16), z(2, 4, 2)
+    ws = z(8, dtype=torch.uint8)
+    good = dict(x=x, gamma=v, beta=v, y=y, stats=stats)
+    bad = [("x", z(24 * 32 - 17, dtype=b16)), ("x", z(24, 32)), ("y", z(24, 15, dtype=b16)),
+           ("gamma", z(15)), ("beta", z(16, dtype=b16)), ("stats", z(15)),
+           ("y", torch.zeros(24, 16, dtype=b16))]
+    for what, t in bad:
+        with pytest.raises(ValueError, match=what):
+            cv.conv3d_group_norm_train_fwd(d, workspace=ws, workspace_bytes=8, stream=0,
+                                           **{**good, what: t})
+        if what != "y":
+            args = {**good, what: t}
+            args["dy"] = args.pop("y")
+            with pytest.raises(ValueError, match=what):
+                cv.conv3d_group_norm_train_bwd(d, dx=None, dgamma=v, dbeta=None, workspace=ws,
+                                               workspace_bytes=8, stream=0, **args)
+    with pytest.raises(ValueError, match="workspace"):
+        cv.conv3d_group_norm_train_fwd(d, workspace=ws, workspace_bytes=9, stream=0, **good)
+    a = z(2, 16, dtype=b16)
+    for what, t in (("dy", z(31, dtype=b16)), ("gamma", z(16)), ("dgamma", z(15)),
+                    ("dvalue", z(2, 16))):
+        args = {**dict(value=a, dy=a, dskip=None, gamma=z(16, dtype=b16), dvalue=a, dgamma=v,
+                       dbias=None), what: t}
+        with pytest.raises(ValueError, match=what):
+            cv.conv3d_norm_silu_bwd(n=1, d=1, h=1, w=2, c=16, workspace=ws, workspace_bytes=8,
+                                    stream=0, **args)
+    for t, elt in ((z(9), cv.ELT_FP32), (z(10), cv.ELT_FP16)):
+        with pytest.raises(ValueError, match="gradient"):
+            cv.make_grads([(t, None, 10, elt, elt)])
+    table = cv.make_grads([(z(10), None, 10, cv.ELT_FP32, cv.ELT_FP32)])
+    for f in (lambda **kw: cv.conv3d_grad_clip(table, 0, 1.0, stream=0, **kw),
+              lambda **kw: cv.conv3d_grad_norm(table, 0, stream=0, **kw)):
+        with pytest.raises(ValueError, match="norm"):
+            f(norm=z(1, dtype=b16), workspace=ws, workspace_bytes=8)
+        with pytest.raises(ValueError, match="workspace"):
+            f(norm=z(1), workspace=ws, workspace_bytes=9)
