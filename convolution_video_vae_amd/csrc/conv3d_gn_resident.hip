@@ -14,7 +14,7 @@
 // write-back then competes with the loads (H3 L0 forward 134 -> 128 us,
 // backward 218 -> 209 us when this came in). So are results stored that would
 // fill half of that cache and more (128 -> 121 and 209 -> 205 us); smaller ones
-// stay there for their reader. H3 L0 now: 121 and 193 us, 91 and 86 % of a
+// stay there for their reader. H3 L0 now: 121 and 193 us, 92 and 86 % of a
 // copy's rate.
 //
 // The exchange. Each piece publishes one 64-bit word per group (two fp32
