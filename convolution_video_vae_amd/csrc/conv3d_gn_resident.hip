@@ -453,12 +453,19 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
   }
   const int c0 = h.range * r.Cb + h.cv * VEC, gl0 = h.cv * VEC;
   const long long at = (long long)h.u * a.P;
+  Samples<T> near;
+  near.load((const E*)a.x + at * a.x_pitch + h.range * r.Cb +
+                min((int)threadIdx.x, r.Gb - 1) * a.cpg,
+            a.P, a.x_pitch, a.cpg);
   long long first;
   const int n = rows_of(a, r, h, h.w, &first);
   Held<T> v[R];
 
   // Per channel, sums about the thread's first value (no cancellation where
-  // the mean is far above the spread) -> the piece's group moments as words.
+  // the mean is far above the spread) -> the piece's group moments as words,
+  // the mean from the group's reference value on (in gmean until the mean is
+  // known): joined as they are, means far above the spread would take a
+  // rounding of their own size at every join.
   // rows(f) visits the thread's rows of the piece, use(g, word) takes the words.
   const auto piece = [&](int n, const Held<T>& v0, auto rows, auto use) {
     float sh[VEC], s1[VEC], s2[VEC];
@@ -477,10 +484,13 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
     });
     Moments m[VEC];
     const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
+    int c = gl0;
+    asm("" : "+v"(c));     // the groups are found again below: kept, they would spill rows
+    GroupOf go(c, a.cpg);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-      const float d = s1[j] * inv;
-      m[j].mean = n > 0 ? sh[j] + d : 0.0f;
+      const float d = s1[j] * inv, ref = gmean[go.next(a.cpg)];
+      m[j].mean = n > 0 ? (sh[j] - ref) + d : 0.0f;
       m[j].m2 = fmaf(-d, s1[j], s2[j]);
       m[j].m2 = m[j].m2 < 0.0f ? 0.0f : m[j].m2;      // and not fmaxf: a NaN stays
     }
@@ -497,13 +507,14 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
       p += step;
     }
   }
+  if (threadIdx.x < r.Gb) gmean[threadIdx.x] = near.reference();
   // pieces joined by the sums of n mean and of squares + n mean^2
   const double full = (double)r.piece_px * a.cpg;
   const double last = (double)(a.P - (long long)(r.W - 1) * r.piece_px) * a.cpg;
   const double inv_n = 1.0 / ((double)a.P * a.cpg);
   const auto group = [&](int g, double s1, double s2) {
     const double mean = s1 * inv_n, var = s2 * inv_n - mean * mean;
-    gmean[g] = (float)mean;
+    gmean[g] = (float)((double)gmean[g] + mean);
     grstd[g] = (float)(1.0 / sqrt((var < 0.0 ? 0.0 : var) + (double)a.eps));  // a NaN stays
   };
   piece(
@@ -514,6 +525,7 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
           if (i < n) f(v[i]);
           if (i < LROWS) lds_x[i][threadIdx.x] = v[i].v;
         }
+        __syncthreads();   // gmean
       },
       [&](int g, unsigned long long word) {
         if (r.W > 1) {

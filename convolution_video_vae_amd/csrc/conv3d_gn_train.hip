@@ -27,9 +27,10 @@
 // No atomics: results do not depend on the order of work-groups.
 //
 // Variance: each thread shifts its channels by the first value it meets, so
-// its fp32 sums hold the spread and not the mean; the shift is taken back in
-// fp64 (x = shift + d: sum x = n shift + sum d, sum x^2 = n shift^2 +
-// 2 shift sum d + sum d^2).
+// its fp32 sums hold the spread and not the mean. The sums that it leaves are
+// about ref, the group's first value (x - ref = shift - ref + d, in fp64): about
+// zero, a constant group of 30000 would have a variance of 1e-7 instead of 0,
+// which is 1e-2 of eps.
 //
 // Vectors: a thread always holds the same VEC elements of a row, so its
 // channels' constants stay in registers. A row is one pixel where VEC
@@ -139,6 +140,12 @@ __device__ __forceinline__ void store_pack(void* p, const Pack<T, VEC>& v) {
     *(Pack<T, VEC>*)p = v;
 }
 
+// The first value of a unit and group.
+template <class T>
+__device__ __forceinline__ float group_ref(const GnTrainArgs& a, int u, int g) {
+  return T::get(((const typename T::store*)a.x)[(long long)u * a.P * a.x_pitch + g * a.cpg]);
+}
+
 template <class T, int VEC>
 __global__ __launch_bounds__(kThreads) void gn_train_stats_kernel(GnTrainArgs a, Rows r) {
   typedef typename T::store E;
@@ -152,9 +159,12 @@ __global__ __launch_bounds__(kThreads) void gn_train_stats_kernel(GnTrainArgs a,
     const long long pitch = r.sp * a.x_pitch;
     const E* x = (const E*)a.x + (long long)u * a.P * a.x_pitch + l.cv * VEC;
     const long long q0 = k * r.chunk_q + l.pl, q1 = min(r.Q, (k + 1) * r.chunk_q);
-    float sh[VEC], s1[VEC], s2[VEC];
+    float ref[VEC], sh[VEC], s1[VEC], s2[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) sh[j] = s1[j] = s2[j] = 0.0f;
+    for (int j = 0; j < VEC; ++j) {
+      ref[j] = group_ref<T>(a, u, channel<VEC>(a, l.cv, j) / a.cpg);
+      sh[j] = s1[j] = s2[j] = 0.0f;
+    }
     if (q0 < q1) unpack<T, VEC>(*(const Pack<T, VEC>*)(x + q0 * pitch), sh);
     Pack<T, VEC> v[U];
     each_row<U>(
@@ -173,7 +183,7 @@ __global__ __launch_bounds__(kThreads) void gn_train_stats_kernel(GnTrainArgs a,
     const double n = q0 < q1 ? (double)((q1 - q0 + r.ppi - 1) / r.ppi) : 0.0;
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-      const double s = sh[j];
+      const double s = (double)sh[j] - (double)ref[j];
       t1[j] = n * s + s1[j];
       t2[j] = n * s * s + 2.0 * s * s1[j] + s2[j];
     }
@@ -200,8 +210,10 @@ __device__ __forceinline__ void block_sum(double& v1, double& v2) {
 }
 
 // One work-group per (unit, group).
+template <class T>
 __global__ __launch_bounds__(kThreads) void gn_train_stats_finalize_kernel(GnTrainArgs a) {
   const int u = blockIdx.x / a.G, g = blockIdx.x - u * a.G;
+  const float ref = group_ref<T>(a, u, g);
   const double* part = a.partial + ((long long)u * a.chunks * a.C + g * a.cpg) * 2;
   double s1 = 0.0, s2 = 0.0;
   const long long n = (long long)a.chunks * a.cpg;
@@ -213,10 +225,10 @@ __global__ __launch_bounds__(kThreads) void gn_train_stats_finalize_kernel(GnTra
   block_sum(s1, s2);
   if (threadIdx.x == 0) {
     const double N = (double)a.P * a.cpg;
-    const double mean = s1 / N;
-    double var = s2 / N - mean * mean;
+    const double off = s1 / N;
+    double var = s2 / N - off * off;
     if (var < 0.0) var = 0.0;                   // and not fmax: a NaN stays
-    a.stats[(long long)blockIdx.x * 2] = (float)mean;
+    a.stats[(long long)blockIdx.x * 2] = (float)((double)ref + off);
     a.stats[(long long)blockIdx.x * 2 + 1] = (float)(1.0 / sqrt(var + (double)a.eps));
   }
 }
@@ -472,7 +484,7 @@ template <class T, int VEC>
 int run_fwd(const GnTrainArgs& a, const Rows& r, hipStream_t s) {
   const dim3 grid((unsigned)a.units * (unsigned)a.chunks, r.tiles);
   hipLaunchKernelGGL((gn_train_stats_kernel<T, VEC>), grid, dim3(kThreads), 0, s, a, r);
-  hipLaunchKernelGGL(gn_train_stats_finalize_kernel, dim3((unsigned)a.units * (unsigned)a.G),
+  hipLaunchKernelGGL((gn_train_stats_finalize_kernel<T>), dim3((unsigned)a.units * (unsigned)a.G),
                      dim3(kThreads), 0, s, a);
   const bool stream = a.stream && kStreams<T, VEC>;
   if (a.silu) start_apply<T, VEC, true>(a, r, grid, stream, s);
