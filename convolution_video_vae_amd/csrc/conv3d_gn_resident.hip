@@ -577,9 +577,9 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
     }
   }
   if (!h.active) return;
-  // 16-bit types: one product per value, x scale + (beta - mean scale); its
-  // roundings are 2^-24 of x's own, x holds 8 or 11 bits. fp32: the
-  // difference from the mean first.
+  // The difference from the mean first: x scale + (beta - mean scale) in one
+  // product would leave a rounding of mean scale, and scale is 316 gamma in a
+  // constant group (H3 L0 123.4 instead of 122.4 us).
   float mean[VEC], scale[VEC], beta[VEC];
   GroupOf go(gl0, a.cpg);
 #pragma unroll
@@ -588,7 +588,6 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
     mean[j] = gmean[g];
     scale[j] = grstd[g] * lgamma[gl0 + j];
     beta[j] = lbeta[gl0 + j];
-    if (!T::kWide) beta[j] = fmaf(-mean[j], scale[j], beta[j]);
   }
   E* y = (E*)a.out + (at + first) * a.out_pitch + c0;
   const long long step = r.ppi * a.out_pitch;
@@ -600,7 +599,7 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
       v[i].get(f);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        f[j] = fmaf(T::kWide ? f[j] - mean[j] : f[j], scale[j], beta[j]);
+        f[j] = fmaf(f[j] - mean[j], scale[j], beta[j]);
         if (SILU && T::kWide) f[j] = silu_of<true>(f[j]);
       }
       if (SILU && !T::kWide) {
@@ -624,24 +623,26 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
   }
 }
 
-// h and da of a vector from its channels' constants. 16-bit types: h =
-// x rstd - mean rstd in one product, a sigmoid's argument straight in powers
-// of two (p = -a log2 e), and 1 + a (1 - sigmoid) from p. fp32: as the
-// formulas say.
+// h and da of a vector from its channels' constants. 16-bit types: a sigmoid's
+// argument straight in powers of two (p = -a log2 e), and 1 + a (1 - sigmoid)
+// from p. fp32: as the formulas say. The difference from the mean always comes
+// first: x rstd - mean rstd in one product would leave a rounding of mean rstd,
+// and in a constant group, where h is 0, nothing else (it cost 98.5 instead of
+// 95 us on [1,17,128,128,256] fp16, 195.8 instead of 192.8 on
+// [1,17,256,256,128] bf16, to do without).
 template <class T, bool SILU, int VEC, int GV>
 struct BwdValues {
   float mean[GV], rstd[GV], gamma[VEC], beta[VEC];
   static constexpr int at(int j) { return j * GV / VEC; }
   __device__ __forceinline__ void init(int j, float m, float s, float g, float b) {
     constexpr float kLog2e = 1.44269502162933349609375f;
-    mean[at(j)] = T::kWide ? m : -m * s;
+    mean[at(j)] = m;
     rstd[at(j)] = s;
     gamma[j] = T::kWide ? g : -g * kLog2e;
     beta[j] = T::kWide ? b : -b * kLog2e;
   }
   __device__ __forceinline__ float h(int j, float x) const {
-    return T::kWide ? mul_alone(x - mean[at(j)], rstd[at(j)])
-                    : fmaf(x, rstd[at(j)], mean[at(j)]);
+    return mul_alone(x - mean[at(j)], rstd[at(j)]);
   }
   // x becomes h, dy becomes da
   __device__ __forceinline__ void run(float (&x)[VEC], float (&dy)[VEC]) const {
@@ -841,15 +842,13 @@ __global__ __launch_bounds__(kGnResThreadsBwd, 2) void gn_resident_bwd_kernel(Gn
     c2[j] = g2[g];
     gam[j] = lgamma[gl0 + j];
     if (!FEW) {
-      // dx = (rstd gamma) da - (rstd c2) h - rstd c1; 16-bit types: h spelt out in x
+      // dx = (rstd gamma) da - (rstd c2) h - rstd c1; 16-bit types: h spelt out
+      // as (x - mean) rstd
       const float rs = bv.rstd[bv.at(j)];
       gam[j] = rs * gam[j];
       c2[j] = -rs * c2[j];
       c1[j] = -rs * c1[j];
-      if (!T::kWide) {
-        c1[j] = fmaf(bv.mean[bv.at(j)], c2[j], c1[j]);
-        c2[j] = rs * c2[j];
-      }
+      if (!T::kWide) c2[j] = rs * c2[j];
     }
   }
   E* dx = (E*)a.out + (at + first) * a.out_pitch + c0;
@@ -878,7 +877,7 @@ __global__ __launch_bounds__(kGnResThreadsBwd, 2) void gn_resident_bwd_kernel(Gn
           f[j] = gn_dx(bv.rstd[bv.at(j)], gam[j], d[j], c1[j], vh[FEW ? i : 0][j], c2[j]);
         else
           f[j] = fmaf(d[j], gam[j],
-                      fmaf(T::kWide ? bv.h(j, f[j]) : f[j], c2[j], c1[j]));
+                      fmaf(T::kWide ? bv.h(j, f[j]) : f[j] - bv.mean[bv.at(j)], c2[j], c1[j]));
       }
       Held<T> o;
       o.put(f);

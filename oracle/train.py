@@ -36,12 +36,10 @@ def group_norm_fwd(x, groups, gamma, beta, *, eps, silu, t_isolated, k=128):
     b4 = np.asarray(beta, np.float64).reshape(1, 1, groups, -1)
     a = h * g4 + b4
     # the mean is off by k roundings of the mean distance from a thread's first
-    # value (at most the group's widest one); rstd by k roundings of the
-    # squares' mean about that value. The mean is rounded to fp32, and a may be
-    # formed as x scale + (beta - mean scale): a rounding of scale, of mean
-    # scale and of the sum, each relative to |mean| scale at most
+    # value (at most the group's widest one), and itself rounded to fp32; rstd
+    # by k roundings of the squares' mean about that value
     spread = np.abs(xg - mean).max(axis=(1, 3), keepdims=True)
-    dm = k * EPS32 * 2.0 * spread + 6 * EPS32 * np.abs(mean)
+    dm = k * EPS32 * 2.0 * spread + 2 * EPS32 * np.abs(mean)
     dr = k * EPS32 * 4.0 * spread ** 2 * rstd ** 2 + 4 * EPS32
     tol = np.abs(g4) * (dm * rstd + np.abs(h) * (dr + 8 * EPS32)) + 4 * EPS32 * np.abs(b4)
     y = a
@@ -74,10 +72,9 @@ def group_norm_bwd(dy, x, groups, gamma, beta, stats, *, silu, t_isolated, k=128
     c1 = (g4 * db).sum(axis=3, keepdims=True) / N
     c2 = (g4 * dgm).sum(axis=3, keepdims=True) / N
     dx = rstd * (g4 * da - c1 - h * c2)
-    # h: two roundings of x - mean and the product, or of mean rstd and of x
-    # rstd - mean rstd; a: two more; da through a slope whose own slope is at
-    # most 1/2, and 8 roundings of the slope
-    dh = 4 * EPS32 * (np.abs(h) + np.abs(mean) * rstd)
+    # h: two roundings of x - mean and the product; a: two more; da through a
+    # slope whose own slope is at most 1/2, and 8 roundings of the slope
+    dh = 4 * EPS32 * np.abs(h)
     dda = np.zeros_like(h)
     if silu:
         dda = np.abs(dg) * (0.5 * (np.abs(g4) * dh + 4 * EPS32 * (np.abs(h * g4) + np.abs(b4)))

@@ -94,3 +94,42 @@ def test_statistics_of_nearly_constant_groups(shape, groups, t_iso, dtype, value
                   <= EPS32 * (np.abs(ref[..., 0]) + 256 * spread))
     rel = EPS32 * (4 + 512 * (spread * ref[..., 1]) ** 2)
     assert np.all(np.abs(got[..., 1] - ref[..., 1]) <= rel * ref[..., 1])
+
+
+@PLACES
+@pytest.mark.parametrize("value", [0.625, -10.0, 1000.0, 30000.0])
+@DTYPES
+@SHAPED
+def test_constant_groups(shape, groups, t_iso, dtype, value, place):
+    n = 2 * (shape[4] // groups)
+    x, _ = constant(shape, groups, dtype, value)
+    dy = draw(shape, dtype, 2, 0.1)
+    op, xd, gamma, beta, y, stats = forward(x, groups, t_iso, False, place)
+    assert torch.equal(y[..., :n].cpu(), beta[:n].to(dtype).expand(*shape[:4], -1))
+    dx, dg, db = op.backward(place(dy), xd, gamma.cuda(), beta.cuda(), stats)
+    assert torch.all(dg[:n] == 0)
+    (rx, rg, rb), (tx, tg, tb) = train.group_norm_bwd(
+        np64(dy), np64(x), groups, np64(gamma), np64(beta), np64(stats), silu=False, t_isolated=t_iso)
+    check(dx, rx, tx, "dx")
+    check(dg, rg, tg, "dgamma")
+    check(db, rb, tb, "dbeta")
+
+
+@PLACES
+@pytest.mark.parametrize("value", [10.0, 1000.0, 30000.0])
+@DTYPES
+@SHAPED
+def test_nearly_constant_groups(shape, groups, t_iso, dtype, value, place):
+    x = nearly_constant(shape, dtype, value)
+    dy = draw(shape, dtype, 5, 0.1)
+    op, xd, gamma, beta, y, stats = forward(x, groups, t_iso, True, place)
+    kw = dict(silu=True, t_isolated=t_iso)
+    ry, _, ty = train.group_norm_fwd(np64(x), groups, np64(gamma), np64(beta),
+                                     eps=float(np.float32(EPS)), **kw)
+    check(y, ry, ty, "y")
+    dx, dg, db = op.backward(place(dy), xd, gamma.cuda(), beta.cuda(), stats)
+    (rx, rg, rb), (tx, tg, tb) = train.group_norm_bwd(
+        np64(dy), np64(x), groups, np64(gamma), np64(beta), np64(stats), **kw)
+    check(dx, rx, tx, "dx")
+    check(dg, rg, tg, "dgamma")
+    check(db, rb, tb, "dbeta")
