@@ -238,3 +238,40 @@ def test_graph_replays_and_repeats_bit_for_bit():
         torch.cuda.synchronize()
         assert torch.equal(norm, want)
         assert all(torch.equal(a, b) for a, b in zip(outs, copies))
+
+
+@pytest.mark.parametrize("calls", [0, 1, 3])
+def test_shortened_and_retyped_tensors_at_their_old_address(calls):
+    """What lies behind a tensor cut short is neither summed nor scaled, and
+    its bytes are read as the type they now have."""
+    whole = draw(4096, torch.float32, 3).cuda()
+    before = whole.cpu()
+    t, other = whole.view(-1), draw(70, torch.bfloat16, 4).cuda()
+    op = GradClip([other, t])
+    for _ in range(calls):
+        op.norm()
+    t.data = t.data[:1000]
+    kept = [np64(other), np64(t)]
+    want = norm_of(kept, "l2")
+    assert abs(op.norm().item() - want) <= 2.0 ** -23 * want
+    op.clip(1.0)
+    check(whole[:1000], before[:1000], 1.0 / (want + 1e-6), "in front")
+    assert torch.equal(whole[1000:].cpu(), before[1000:])
+    bits = whole[:500].cpu().view(torch.bfloat16)
+    other.data = torch.zeros(1, dtype=torch.bfloat16, device="cuda")
+    whole[:500] = torch.ones(1000, dtype=torch.bfloat16).view(torch.float32).cuda()
+    t.data = whole[:500].view(torch.bfloat16)
+    assert bits.numel() == t.numel() == 1000
+    assert abs(op.norm().item() - math.sqrt(1000.0)) <= 2.0 ** -23 * 32
+
+
+def test_a_storage_cut_short_is_refused():
+    t = torch.full((4096,), 2.0, device="cuda")
+    op = GradClip([t])
+    assert op.norm().item() == 128.0
+    t.untyped_storage().resize_(0)
+    with pytest.raises(ValueError, match="storage"):
+        op.norm()
+    t.untyped_storage().resize_(1024)
+    with pytest.raises(ValueError, match="storage"):
+        op.clip(1.0)
