@@ -19,7 +19,9 @@
 // (an fp32 square leaves the range from |g| > 1.8e19 and < 1e-23); each
 // work-group leaves one partial, and every work-group of the clip pass adds
 // all of them in the same fixed order, so no launch stands between the two
-// passes and the result does not depend on the order of work-groups.
+// passes and the result does not depend on the order of work-groups. Every
+// tensor leaves a partial, and that work grows with their square: of many, one
+// work-group adds them (in that order, to the same value) between the passes.
 #include <hip/hip_runtime.h>
 
 #include "conv3d_device.h"
@@ -121,17 +123,22 @@ __global__ __launch_bounds__(kThreads) void grad_partials_kernel(GradBatch b) {
 }
 
 template <bool INF>
-__device__ __forceinline__ double total_norm(const GradBatch& b) {
+__device__ __forceinline__ double join_partials(const GradBatch& b) {
   double acc = 0.0;
   for (int i = threadIdx.x; i < b.partials; i += kThreads) acc = merge<INF>(acc, b.all[i]);
-  acc = block_merge<INF>(acc);
-  return INF ? acc : sqrt(acc);
+  return block_merge<INF>(acc);
+}
+template <bool INF>
+__device__ __forceinline__ double norm_of(double join) {
+  return INF ? join : sqrt(join);
 }
 
 template <bool INF>
 __global__ __launch_bounds__(kThreads) void grad_norm_kernel(GradBatch b) {
-  const double n = total_norm<INF>(b);
-  if (threadIdx.x == 0) *b.norm = (float)n;
+  const double join = join_partials<INF>(b);
+  if (threadIdx.x) return;
+  if (b.join) *b.join = join;
+  *b.norm = (float)norm_of<INF>(join);
 }
 
 // A lane's vector of results; STREAM: past the caches (16 bytes, or 8 where the
@@ -197,7 +204,7 @@ __device__ __forceinline__ void scale_to(const void* src, void* dst, int out, lo
 
 template <bool INF, bool STREAM>
 __global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradBatch b) {
-  const double norm = total_norm<INF>(b);
+  const double norm = norm_of<INF>(join_partials<INF>(b));
   if (b.norm && blockIdx.x == 0 && threadIdx.x == 0) *b.norm = (float)norm;
   const double c = (double)b.max_norm / (norm + 1e-6);
   const float coef = c > 1.0 ? 1.0f : (float)c;      // a NaN is not above 1

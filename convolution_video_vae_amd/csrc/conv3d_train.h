@@ -93,7 +93,8 @@ constexpr int kGradItems = 120;          // 32 bytes each: the arguments stay be
 struct GradBatch {
   GradItem item[kGradItems];
   double* partial;           // of this batch's first block (norm pass)
-  const double* all;         // every batch's partials (clip pass)
+  const double* all;         // every batch's partials, or their join (clip pass)
+  double* join;              // norm kernel: the join of all partials, or null
   float* norm;
   int count;                 // tensors in this batch
   int blocks;                // blocks of this batch

@@ -430,6 +430,13 @@ long long grad_chunk(long long total) {
   return std::max(kGradMinChunk, (std::min(few, many) + kGradStep) / kGradStep * kGradStep);
 }
 
+// Partials up to which every work-group of the clip pass adds them by itself:
+// more than large tensors leave (some 2000). Of more, a launch between the
+// passes adds them once (n tensors of 64 values, one partial each, by
+// themselves and by a launch: 500 33 and 34 us, 2000 107 and 95, 4000 234 and
+// 181, 32000 4822 and 1360).
+constexpr long long kGradDirect = 2560;
+
 long long grad_blocks(long long numel, long long chunk) { return (numel + chunk - 1) / chunk; }
 
 conv3d_status plan_grads(const conv3d_grad* g, int count, GradPlan* pl) {
@@ -446,7 +453,8 @@ conv3d_status plan_grads(const conv3d_grad* g, int count, GradPlan* pl) {
   pl->chunk = grad_chunk(total);
   for (int i = 0; i < count; ++i) pl->partials += grad_blocks(g[i].numel, pl->chunk);
   if (pl->chunk > (1LL << 30) || pl->partials > (1LL << 24) - 1) return CONV3D_ERR_UNSUPPORTED;
-  pl->bytes = ((size_t)std::max(pl->partials, 1LL) * 8 + 255) / 256 * 256;
+  // the partials, and behind them their join
+  pl->bytes = ((size_t)(pl->partials + 1) * 8 + 255) / 256 * 256;
   return CONV3D_OK;
 }
 
@@ -526,6 +534,13 @@ conv3d_status run_grads(const conv3d_grad* g, int count, int norm_type, bool cli
     b.partial = partial;
     b.norm = norm;
     b.count = b.blocks = 0;
+    if (pass == 1 && pl.partials > kGradDirect) {
+      b.join = partial + pl.partials;
+      if (launch_grad_norm(b, stream)) return CONV3D_ERR_HIP;
+      b.all = b.join;
+      b.partials = 1;
+      b.norm = nullptr;
+    }
     for (int i = 0; i < count; ++i) {
       if (g[i].numel == 0) continue;
       GradItem& it = b.item[b.count++];

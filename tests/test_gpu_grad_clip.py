@@ -275,3 +275,23 @@ def test_a_storage_cut_short_is_refused():
     t.untyped_storage().resize_(1024)
     with pytest.raises(ValueError, match="storage"):
         op.clip(1.0)
+
+
+@pytest.mark.parametrize("kind", ["l2", "inf"])
+@pytest.mark.parametrize("count", [2560, 2561, 9000])
+def test_many_tensors(count, kind):
+    """Lists on both sides of the number of partials that the clip pass's
+    work-groups add by themselves; the norm is the norm call's, bit for bit."""
+    g = torch.Generator().manual_seed(count)
+    flat = torch.randn(count * 24, generator=g)
+    if kind == "inf":
+        flat[count * 11] = 77.0
+    dev = flat.cuda()
+    op = GradClip(list(dev.split(24)), norm=kind)
+    want = norm_of([np64(flat)], kind)
+    first = op.norm()
+    got = op.clip(want / 4)
+    assert torch.equal(first, got) and abs(got.item() - want) <= 2.0 ** -23 * want
+    check(dev, flat, float(np.float32(want / 4)) / (want + 1e-6), "gradients")
+    dev[5] = float("nan")
+    assert math.isnan(op.clip(1.0).item()) and torch.isnan(dev).all()
