@@ -194,21 +194,27 @@ int launch_ns_bwd(const NsBwdArgs& a, void* stream) {
   hipStream_t s = (hipStream_t)stream;
   (void)hipGetLastError();
   const int V = a.C / 8, g = lanes_per_row(a.C), k = (V + g - 1) / g;
+  // lanes_per_row leaves no other pairs
 #define CONV3D_NS_CASE(G)                       \
   case G:                                       \
-    if (k == 1) launch<G, 1>(a, s);             \
-    else if (k == 2) launch<G, 2>(a, s);        \
-    else if (k == 3) launch<G, 3>(a, s);        \
-    else launch<G, 4>(a, s);                    \
+    if (k == 2) launch<G, 2>(a, s);             \
+    else launch<G, 3>(a, s);                    \
     break;
   switch (g) {
-    CONV3D_NS_CASE(1)
+    case 1:
+      if (k == 1) launch<1, 1>(a, s);
+      else if (k == 2) launch<1, 2>(a, s);
+      else launch<1, 3>(a, s);
+      break;
     CONV3D_NS_CASE(2)
     CONV3D_NS_CASE(4)
     CONV3D_NS_CASE(8)
     CONV3D_NS_CASE(16)
     CONV3D_NS_CASE(32)
-    CONV3D_NS_CASE(64)
+    default:
+      if (k == 2) launch<64, 2>(a, s);
+      else if (k == 3) launch<64, 3>(a, s);
+      else launch<64, 4>(a, s);
   }
 #undef CONV3D_NS_CASE
   if (a.dgamma || a.dbias)
