@@ -94,7 +94,8 @@ __device__ __forceinline__ void Held<Bf16>::put(const float (&f)[8]) {
 // exponential; it overflows to infinity below a = -88, where 1 / (1 + t) = 0 is
 // the rounded value anyway. fp32 results (EXACT): the rounding of a log2 e is
 // made good by a second product, and only e^-|a| is formed, so that 1 - sig
-// needs no difference. A NaN stays in both.
+// needs no difference. A NaN stays one only where it is multiplied with: here
+// the fp32 form makes it 0, and both uses below multiply by the argument.
 template <bool EXACT>
 __device__ __forceinline__ float exp_neg(float v) {
   constexpr float kLog2e = 1.44269502162933349609375f;

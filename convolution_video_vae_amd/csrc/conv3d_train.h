@@ -84,7 +84,7 @@ int launch_ns_bwd(const NsBwdArgs& args, void* stream);
 // Gradient norm and clipping (conv3d_grad_clip.hip).
 struct GradItem {
   const void* src;
-  void* dst;                 // null in the norm pass
+  void* dst;                 // where the clip pass writes (src: in place)
   long long numel;
   int first;                 // the first block of this tensor in its launch
   short dtype, out_dtype;
