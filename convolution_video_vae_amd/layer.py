@@ -213,7 +213,8 @@ class GroupNorm:
 # The classes below run on the current stream of their tensors' device.
 # Outputs and scratch memory that a call needs come from PyTorch's allocator
 # on that stream (inside a graph capture, from the graph's own pool), so one
-# object may serve several streams and graphs at once.
+# object may serve several streams and graphs at once. Autograd does not record
+# these calls: results carry no graph, whatever their inputs require.
 
 # The current stream's handle without a Stream object around it (3 us less per call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -475,7 +476,9 @@ class GradClip:
     types). The lists are kept, and so is the memory that the tensors had at
     the last call: a tensor whose address, type, size or strides have changed
     since (`t.data = ...`) is looked up again, and none moves to where another
-    was."""
+    was. For gradients that stay the same tensors from step to step; where each
+    step makes new ones (`zero_grad()` sets .grad to None), these here would be
+    the old ones, still held: call clip_grads."""
 
     def __init__(self, grads: Sequence[torch.Tensor],
                  outs: Optional[Sequence[torch.Tensor]] = None, *, norm: str = "l2"):
@@ -577,5 +580,6 @@ class GradClip:
 
 
 def clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *, norm: str = "l2") -> torch.Tensor:
-    """Clips gradients in place by their global norm and returns it."""
+    """Clips gradients in place by their global norm and returns it; nothing is
+    kept of the list."""
     return GradClip(grads, norm=norm)._clip(max_norm, fresh=True)

@@ -441,7 +441,10 @@ conv3d_status conv3d_group_norm_train_bwd(const conv3d_group_norm_train_desc* de
  *   dgamma[c] = sum over the pixels of da * e, dbias[c] = of dvalue before B
  * in fp32, without the forward pass's intermediate roundings. dvalue is the
  * gradient of the conv's output and of the residual; dskip (or NULL) is the
- * gradient that reaches `value` past the norm, through residual_out.
+ * gradient that reaches `value` past the norm, through residual_out. A layer
+ * without a residual (the fused conv writes residual_out only with one) runs
+ * the conv without the norm and conv3d_norm_silu on its output, which is
+ * `value` then.
  *   value, dy, dskip, dvalue  bf16 NDHWC [n][d][h][w][c], gamma bf16 [c]
  *   dgamma, dbias             fp32 [c], overwritten; each may be NULL
  *   workspace                 conv3d_norm_silu_bwd_workspace_bytes; may be
