@@ -12,29 +12,23 @@ __device__ __forceinline__ double wave_sum(double v) {
   return v;
 }
 
-// A value that the group's are counted from, out of four of them: the one of
-// least magnitude, or 0 where their signs differ. Where all values lie far from
-// zero it is one of them, and what is left is of the size of their spread; an
-// outlier is not taken. x: the group's first value in its unit, of P pixels and
-// cpg channels.
+// A value that the group's are counted from: of its first and one in its middle
+// the one of lesser magnitude (an outlier among them is not taken), or 0 where
+// their signs differ. It lies between the group's least and greatest value, so
+// what is left is of the size of their spread. x: the group's first value in
+// its unit, of P pixels and cpg channels. (Four values: [1,5,16,16,1024] bf16
+// forward 7.7 instead of 7.5 us.)
 template <class T>
 struct Samples {
-  typename T::store v[4];
+  typename T::store v[2];
   __device__ __forceinline__ void load(const typename T::store* x, long long P, long long pitch,
                                        int cpg) {
     v[0] = x[0];
-    v[1] = x[P / 3 * pitch + cpg / 2];
-    v[2] = x[(P - 1 - P / 3) * pitch + cpg / 3];
-    v[3] = x[(P - 1) * pitch + cpg - 1];
+    v[1] = x[P / 2 * pitch + cpg / 2];
   }
   __device__ __forceinline__ float reference() const {
-    float k = T::get(v[0]);
-#pragma unroll
-    for (int i = 1; i < 4; ++i) {
-      const float s = T::get(v[i]);
-      k = (k < 0.0f) != (s < 0.0f) ? 0.0f : fabsf(s) < fabsf(k) ? s : k;
-    }
-    return k;
+    const float k = T::get(v[0]), s = T::get(v[1]);
+    return (k < 0.0f) != (s < 0.0f) ? 0.0f : fabsf(s) < fabsf(k) ? s : k;
   }
 };
 

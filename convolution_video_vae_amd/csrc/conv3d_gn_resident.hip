@@ -344,7 +344,11 @@ __device__ __forceinline__ void each_group(int Gb, int cpg, Value value, Use use
 // reads of the words are contiguous; the threads' sums are joined in order.
 template <int NT>
 struct PieceSums {
-  double a[NT], b[NT];
+  union {
+    double a[NT];
+    f32x4_t ref[NT / 4];         // before the join: the channels' reference values
+  };
+  double b[NT];
   unsigned long long own[NT];    // one piece's words
   int late;
 
@@ -447,24 +451,20 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
   const Where h = where(r);
   // ahead of the rows: a load that is issued later returns after all of them,
   // and after those of the other work-group on this CU
-  if (threadIdx.x < r.Cb) {
-    lgamma[threadIdx.x] = a.gamma[h.range * r.Cb + threadIdx.x];
-    lbeta[threadIdx.x] = a.beta[h.range * r.Cb + threadIdx.x];
-  }
+  const int ct = min((int)threadIdx.x, r.Cb - 1), kg = ct / a.cpg;
+  const float gamma_t = a.gamma[h.range * r.Cb + ct], beta_t = a.beta[h.range * r.Cb + ct];
   const int c0 = h.range * r.Cb + h.cv * VEC, gl0 = h.cv * VEC;
   const long long at = (long long)h.u * a.P;
   Samples<T> near;
-  near.load((const E*)a.x + at * a.x_pitch + h.range * r.Cb +
-                min((int)threadIdx.x, r.Gb - 1) * a.cpg,
-            a.P, a.x_pitch, a.cpg);
+  near.load((const E*)a.x + at * a.x_pitch + h.range * r.Cb + kg * a.cpg, a.P, a.x_pitch, a.cpg);
   long long first;
   const int n = rows_of(a, r, h, h.w, &first);
   Held<T> v[R];
 
   // Per channel, sums about the thread's first value (no cancellation where
   // the mean is far above the spread) -> the piece's group moments as words,
-  // the mean from the group's reference value on (in gmean until the mean is
-  // known): joined as they are, means far above the spread would take a
+  // the mean from the group's reference value on (in gmean too, until the mean
+  // is known): joined as they are, means far above the spread would take a
   // rounding of their own size at every join.
   // rows(f) visits the thread's rows of the piece, use(g, word) takes the words.
   const auto piece = [&](int n, const Held<T>& v0, auto rows, auto use) {
@@ -484,13 +484,13 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
     });
     Moments m[VEC];
     const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
-    int c = gl0;
-    asm("" : "+v"(c));     // the groups are found again below: kept, they would spill rows
-    GroupOf go(c, a.cpg);
+    f32x4_t ref[VEC / 4];
+#pragma unroll
+    for (int j = 0; j < VEC; j += 4) ref[j / 4] = pieces.ref[(gl0 + j) / 4];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-      const float d = s1[j] * inv, ref = gmean[go.next(a.cpg)];
-      m[j].mean = n > 0 ? (sh[j] - ref) + d : 0.0f;
+      const float d = s1[j] * inv, mean = (sh[j] - ref[j / 4][j & 3]) + d;
+      m[j].mean = n > 0 ? mean : 0.0f;
       m[j].m2 = fmaf(-d, s1[j], s2[j]);
       m[j].m2 = m[j].m2 < 0.0f ? 0.0f : m[j].m2;      // and not fmaxf: a NaN stays
     }
@@ -507,12 +507,20 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
       p += step;
     }
   }
-  if (threadIdx.x < r.Gb) gmean[threadIdx.x] = near.reference();
-  // pieces joined by the sums of n mean and of squares + n mean^2
-  const double full = (double)r.piece_px * a.cpg;
-  const double last = (double)(a.P - (long long)(r.W - 1) * r.piece_px) * a.cpg;
-  const double inv_n = 1.0 / ((double)a.P * a.cpg);
+  if (threadIdx.x < r.Cb) {
+    const float k = near.reference();
+    lgamma[threadIdx.x] = gamma_t;
+    lbeta[threadIdx.x] = beta_t;
+    ((float*)pieces.ref)[threadIdx.x] = k;
+    if (threadIdx.x == kg * a.cpg) gmean[kg] = k;
+  }
+  // pieces joined by the sums of n mean and of squares + n mean^2 (the counts
+  // are formed where they are used: six registers less beside the rows)
+  const auto values = [&](int w) {
+    return (double)(w == r.W - 1 ? a.P - (long long)w * r.piece_px : r.piece_px) * a.cpg;
+  };
   const auto group = [&](int g, double s1, double s2) {
+    const double inv_n = 1.0 / ((double)a.P * a.cpg);
     const double mean = s1 * inv_n, var = s2 * inv_n - mean * mean;
     gmean[g] = (float)((double)gmean[g] + mean);
     grstd[g] = (float)(1.0 / sqrt((var < 0.0 ? 0.0 : var) + (double)a.eps));  // a NaN stays
@@ -525,21 +533,21 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
           if (i < n) f(v[i]);
           if (i < LROWS) lds_x[i][threadIdx.x] = v[i].v;
         }
-        __syncthreads();   // gmean
+        __syncthreads();   // pieces.ref
       },
       [&](int g, unsigned long long word) {
         if (r.W > 1) {
           pieces.own[g] = word;
         } else {
-          const double mean = word_lo(word);
-          group(g, mean * last, (double)word_hi(word) + mean * mean * last);
+          const double mean = word_lo(word), N = values(0);
+          group(g, mean * N, (double)word_hi(word) + mean * mean * N);
         }
       });
   __syncthreads();
   if (r.W > 1) {
     double s1 = 0.0, s2 = 0.0;
     const auto add = [&](int w, unsigned long long x) {
-      const double mean = word_lo(x), nm = (w == r.W - 1 ? last : full) * mean;
+      const double mean = word_lo(x), nm = values(w) * mean;
       s1 += nm;
       s2 += (double)word_hi(x) + nm * mean;
     };
@@ -579,7 +587,8 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
   if (!h.active) return;
   // The difference from the mean first: x scale + (beta - mean scale) in one
   // product would leave a rounding of mean scale, and scale is 316 gamma in a
-  // constant group (H3 L0 123.4 instead of 122.4 us).
+  // constant group. (A product costs [1,9,128,128,320] fp16 61.9 instead of 63 us,
+  // H3 L0 nothing.)
   float mean[VEC], scale[VEC], beta[VEC];
   GroupOf go(gl0, a.cpg);
 #pragma unroll
@@ -589,7 +598,12 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
     scale[j] = grstd[g] * lgamma[gl0 + j];
     beta[j] = lbeta[gl0 + j];
   }
-  E* y = (E*)a.out + (at + first) * a.out_pitch + c0;
+  // the thread's place once more: kept since the loads, it spills
+  int t = threadIdx.x;
+  asm("" : "+v"(t));
+  const int pl = t / r.Vb;
+  E* y = (E*)a.out + (at + (long long)h.w * r.piece_px + pl) * a.out_pitch + h.range * r.Cb +
+         (t - pl * r.Vb) * VEC;
   const long long step = r.ppi * a.out_pitch;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
