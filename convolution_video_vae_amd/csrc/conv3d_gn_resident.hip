@@ -14,7 +14,7 @@
 // write-back then competes with the loads (H3 L0 forward 134 -> 128 us,
 // backward 218 -> 209 us when this came in). So are results stored that would
 // fill half of that cache and more (128 -> 121 and 209 -> 205 us); smaller ones
-// stay there for their reader. H3 L0 now: 121 and 193 us, 92 and 86 % of a
+// stay there for their reader. H3 L0 now: 121 and 196 us, 91 and 85 % of a
 // copy's rate.
 //
 // The exchange. Each piece publishes one 64-bit word per group (two fp32
@@ -641,9 +641,9 @@ __global__ __launch_bounds__(kGnResThreadsFwd, 4) void gn_resident_fwd_kernel(Gn
 // argument straight in powers of two (p = -a log2 e), and 1 + a (1 - sigmoid)
 // from p. fp32: as the formulas say. The difference from the mean always comes
 // first: x rstd - mean rstd in one product would leave a rounding of mean rstd,
-// and in a constant group, where h is 0, nothing else (it cost 98.5 instead of
-// 95 us on [1,17,128,128,256] fp16, 195.8 instead of 192.8 on
-// [1,17,256,256,128] bf16, to do without).
+// and in a constant group, where h is 0, nothing else. (That product took 95 us
+// instead of 98.5 on [1,17,128,128,256] fp16, 193 instead of 196 on
+// [1,17,256,256,128] bf16.)
 template <class T, bool SILU, int VEC, int GV>
 struct BwdValues {
   float mean[GV], rstd[GV], gamma[VEC], beta[VEC];

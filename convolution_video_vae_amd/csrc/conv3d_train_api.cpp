@@ -39,13 +39,13 @@ struct GnTrainPlan {
 
 // Pieces of one exchange: half of the 512 work-groups that the chip holds, so
 // that two calls side by side still find room. (Resident against two passes,
-// backward: [1,8,256,512,128] bf16, 256 pieces, 201 and 257 us; at 384 pieces,
+// backward: [1,8,256,512,128] bf16, 256 pieces, 206 and 257 us; at 384 pieces,
 // [1,4,384,512,128], 182 and 197 us, left to two passes for that room.)
 constexpr int kGnMaxPieces = 256;
 constexpr int kGnFill = 256;             // work-groups that give every CU one
 // Rows per thread up to which one work-group per narrow range is better than
 // an exchange, where the chip is not filled ([1,5,32,32,512] bf16 forward, 8
-// rows: 9.9 and 11.3 us; backward, 16 rows: 20.0 and 14.7 us).
+// rows: 10.6 and 11.9 us; backward, 16 rows: 19.4 and 15.2 us).
 constexpr int kGnAloneRows = 10;
 constexpr int kGnSpin = 5000;            // polls (some 5 ms) before a work-group helps itself
 
